@@ -7,9 +7,12 @@ fails to load, importing this module raises.
 Names mirror the C ABI in ``include/infini_attn.h``:
 ``infini_attn_fwd`` (bf16), ``infini_attn_fwd_f32``, ``infini_attn_workspace_bytes``,
 ``infini_attn_status_string``, ``infini_attn_version``, ``infini_attn_decode_step`` (+
-``_f32``), ``infini_attn_fold`` (+ ``_f32``), ``infini_attn_state`` (+ ``_f32``);
-``forward``, ``decode_step``, ``fold`` and ``state`` allocate what is missing and pick the
-entry point from the activation dtype.
+``_f32``), ``infini_attn_fold`` (+ ``_f32``), ``infini_attn_state`` (+ ``_f32``), and, for
+serving from a paged cache, ``infini_attn_rotary`` / ``_rotary_bwd``, ``_paged_append``,
+``_paged_decode_step`` and ``_paged_evict`` (+ ``_f32`` each);
+``forward``, ``decode_step``, ``fold``, ``state``, ``rotary``, ``rotary_backward``,
+``paged_append``, ``paged_decode_step`` and ``paged_evict`` allocate what is missing and pick
+the entry point from the activation dtype.
 """
 from __future__ import annotations
 
@@ -25,7 +28,8 @@ DELTA = 1
 RULES = {"linear": LINEAR, "delta": DELTA, LINEAR: LINEAR, DELTA: DELTA}
 
 STATUS = {0: "INFINI_OK", 1: "INFINI_ERR_INVALID_ARG", 2: "INFINI_ERR_UNSUPPORTED",
-          3: "INFINI_ERR_CUDA", 4: "INFINI_ERR_OOM", 5: "INFINI_ERR_TIMEOUT"}
+          3: "INFINI_ERR_CUDA", 4: "INFINI_ERR_OOM", 5: "INFINI_ERR_TIMEOUT",
+          6: "INFINI_ERR_PAGE"}
 
 #: C functions and their (argtypes, restype), exactly as include/infini_attn.h declares them
 _P, _I64, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
@@ -34,7 +38,23 @@ _DEC_ARGS = [_P] * 6 + [_I64] + [_P] * 3 + [_I64] * 5 + [_I, _P]
 _FOLD_ARGS = [_P, _P, _I64, _P, _P] + [_I64] * 4 + [_I, _P]
 _STATE_ARGS = [_P] * 6 + [_I64] * 5 + [_I, _P]
 _BWD_ARGS = [_P] * 15 + [_I64] * 6 + [_I, _P]
+_ROT_ARGS = [_P] * 6 + [_I64] + [_P] * 2 + [_I64] * 6 + [_I, ctypes.c_float, _P]
+_APP_ARGS = [_P] * 10 + [_I64] * 7 + [_P]
+_PDEC_ARGS = [_P] * 15 + [_I64] * 9 + [_I, ctypes.c_float, _P]
+_EVICT_ARGS = [_P] * 11 + [_I64] * 10 + [_I, _P]
 SIGNATURES = {
+    "infini_attn_rotary": (_ROT_ARGS, _I),
+    "infini_attn_rotary_f32": (_ROT_ARGS, _I),
+    "infini_attn_rotary_bwd": (_ROT_ARGS, _I),
+    "infini_attn_rotary_bwd_f32": (_ROT_ARGS, _I),
+    "infini_attn_paged_append": (_APP_ARGS, _I),
+    "infini_attn_paged_append_f32": (_APP_ARGS, _I),
+    "infini_attn_paged_decode_step": (_PDEC_ARGS, _I),
+    "infini_attn_paged_decode_step_f32": (_PDEC_ARGS, _I),
+    "infini_attn_paged_decode_workspace_bytes": ([_I64] * 6 + [_I], _I64),
+    "infini_attn_paged_evict": (_EVICT_ARGS, _I),
+    "infini_attn_paged_evict_f32": (_EVICT_ARGS, _I),
+    "infini_attn_paged_evict_workspace_bytes": ([_I64] * 6 + [_I], _I64),
     "infini_attn_fwd": (_FWD_ARGS, _I),
     "infini_attn_fwd_f32": (_FWD_ARGS, _I),
     "infini_attn_fwd_noalloc": (_FWD_ARGS, _I),
@@ -92,7 +112,8 @@ def infini_attn_workspace_bytes(B, Hkv, L, N, d) -> int:
 
 
 def infini_attn_device_status(stream=None) -> int:
-    """Synchronise the stream; INFINI_ERR_TIMEOUT (5) if a bounded device wait gave up."""
+    """Synchronise the stream; INFINI_ERR_TIMEOUT (5) if a bounded device wait gave up,
+    INFINI_ERR_PAGE (6) if a paged call met a page or row outside its cache."""
     return LIB.infini_attn_device_status(_stream_handle(stream))
 
 
@@ -319,3 +340,229 @@ def backward(q, k, v, beta, M0, z0, dout, dM=None, dz=None, *, N: int, rule="lin
     if rc != 0:
         raise InfiniError(rc, infini_attn_status_string(rc))
     return dq, dk, dv, dbeta, dM0, dz0
+
+
+# ---- serving from a paged cache ------------------------------------------------------------
+
+class _Launch:
+    """Device and stream of one call: allocations inside belong to the stream it runs on."""
+
+    def __init__(self, device, stream):
+        if not isinstance(device, torch.device) or device.type != "cuda":
+            raise ValueError("the tensors must be on a CUDA device")
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        self.stream = stream
+        self.guard = None
+        if stream is not None:
+            self.guard = torch.cuda.stream(stream)       # sets the device too
+        elif device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return _stream_handle(self.stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _run(fn, *args):
+    rc = fn(*args)
+    if rc != 0:
+        raise InfiniError(rc, infini_attn_status_string(rc))
+
+
+def _entry(name, dtype):
+    if dtype == torch.bfloat16:
+        return getattr(LIB, name)
+    if dtype == torch.float32:
+        return getattr(LIB, name + "_f32")
+    raise ValueError(f"unsupported activation dtype {dtype}")
+
+
+def _strides(t, name, dtype, shape, device):
+    """Element strides (batch, head, token) of a [B, H, L, d] view with contiguous rows."""
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.stride(3) != 1:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)} with contiguous rows, got "
+                         f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}")
+    B, H, L, d = t.shape
+    s = t.stride()
+    # a dimension of one entry may carry any stride: name the contiguous one
+    return (_I64 * 3)(s[0] if B > 1 else H * L * d, s[1] if H > 1 else L * d, s[2] if L > 1 else d)
+
+
+def _rotary(name, q, k, freq, positions, start, interleaved, scale, q_out, k_out, stream):
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
+        raise ValueError("q and k are [B, H, L, d] and [B, Hkv, L, d]")
+    B, H, L, d = q.shape
+    dev = q.device
+    fn = _entry(name, q.dtype)
+    with _Launch(dev, stream) as handle:
+        sq = _strides(q, "q", q.dtype, (B, H, L, d), dev)
+        Hkv, sk = 0, None
+        if k is not None:
+            Hkv = k.shape[1]
+            sk = _strides(k, "k", q.dtype, (B, Hkv, L, d), dev)
+        elif k_out is not None:
+            raise ValueError("k_out without k")
+        _check(freq, "freq", torch.float64, (freq.numel(),), dev)
+        _check(positions, "positions", torch.int64, (B, L), dev)
+        if q_out is None:
+            q_out = torch.empty((B, H, L, d), dtype=q.dtype, device=dev)
+        if k is not None and k_out is None:
+            k_out = torch.empty((B, Hkv, L, d), dtype=q.dtype, device=dev)
+        _check(q_out, "q_out", q.dtype, (B, H, L, d), dev)
+        _check(k_out, "k_out", q.dtype, (B, Hkv, L, d), dev)
+        _run(fn, _ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(freq), _ptr(positions),
+             int(start), sq, sk, B, H, Hkv, L, d, 2 * freq.numel(), 1 if interleaved else 0,
+             float(scale), handle)
+    return q_out, k_out
+
+
+def rotary(q, k, freq, *, positions=None, start: int = 0, interleaved: bool = False, scale=1.0,
+           q_out=None, k_out=None, stream=None):
+    """Rotary positions for the forward's q [B,H,L,d] and k [B,Hkv,L,d] (bf16 or fp32; k may be
+    None).  Both may be strided views with contiguous rows, such as a token-major projection
+    transposed; the outputs are contiguous.
+
+    freq [rot/2] fp64 on the device (``rotary_frequencies``): the first rot channels turn, pair
+    i by position * freq[i]; pairs are (i, i + rot/2), or (2i, 2i+1) when ``interleaved``.
+    positions [B,L] int64, or None: token t is at ``start + t``.  ``scale`` multiplies the
+    turned channels.  q_out / k_out may be their own contiguous inputs.  Returns (q_out, k_out).
+    """
+    return _rotary("infini_attn_rotary", q, k, freq, positions, start, interleaved, scale, q_out,
+                   k_out, stream)
+
+
+def rotary_backward(dq_out, dk_out, freq, *, positions=None, start: int = 0,
+                    interleaved: bool = False, scale=1.0, dq=None, dk=None, stream=None):
+    """Gradients of ``rotary``'s inputs from those of its outputs (arguments as there)."""
+    return _rotary("infini_attn_rotary_bwd", dq_out, dk_out, freq, positions, start, interleaved,
+                   scale, dq, dk, stream)
+
+
+def _pool(k_pages, v_pages, weights, dev):
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages and v_pages are [P, Hkv, page, d]")
+    shape = tuple(k_pages.shape)
+    _check(k_pages, "k_pages", k_pages.dtype, shape, dev)
+    _check(v_pages, "v_pages", k_pages.dtype, shape, dev)
+    _check(weights, "weights", torch.float32, shape[:3], dev)
+    return shape
+
+
+def _table(page_table, lens, dev, name="page_table"):
+    if page_table.dim() != 2:
+        raise ValueError(f"{name} is [B, pages]")
+    B, pages = page_table.shape
+    _check(page_table, name, torch.int32, (B, pages), dev)
+    _check(lens, "lens", torch.int32, (B,), dev)
+    return B, pages
+
+
+def paged_append(k, v, k_pages, v_pages, page_table, lens, *, counts=None, weights=None,
+                 stream=None):
+    """Write the tokens k/v [B,Hkv,T,d] (strided views allowed) into rows lens[b]..
+    lens[b]+counts[b]-1 of the cache (counts [B] int32, None: T each); their weights start at 0.
+
+    k_pages/v_pages [P,Hkv,page,d] (bf16 or fp32), page_table [B,max_pages] and lens [B] int32,
+    weights [P,Hkv,page] fp32 or None.  lens is left to the caller.
+    """
+    dev = k_pages.device
+    with _Launch(dev, stream) as handle:
+        P, Hkv, page, d = _pool(k_pages, v_pages, weights, dev)
+        B, max_pages = _table(page_table, lens, dev)
+        if k.dim() != 4:
+            raise ValueError("k and v are [B, Hkv, T, d]")
+        T = k.shape[2]
+        sk = _strides(k, "k", k_pages.dtype, (B, Hkv, T, d), dev)
+        sv = _strides(v, "v", k_pages.dtype, (B, Hkv, T, d), dev)
+        _check(counts, "counts", torch.int32, (B,), dev)
+        _run(_entry("infini_attn_paged_append", k_pages.dtype), _ptr(k), _ptr(v), sk, sv,
+             _ptr(k_pages), _ptr(v_pages), _ptr(weights), _ptr(page_table), _ptr(lens),
+             _ptr(counts), B, Hkv, T, d, P, page, max_pages, handle)
+
+
+def paged_decode_step(q, k, v, k_pages, v_pages, page_table, lens, *, beta=None, M=None, z=None,
+                      weights=None, freq=None, positions=None, interleaved: bool = False,
+                      scale=1.0, out=None, stream=None):
+    """One new token of every sequence over its paged cache.
+
+    q [B,H,d], k/v [B,Hkv,d] (bf16 or fp32; k = v = None: attend to the cached rows alone);
+    cache arguments as for ``paged_append``.  With freq [rot/2] fp64, q and k are rotated first,
+    at positions [B] int64 (None: lens).  k, v become row lens[b]; the attention spans rows
+    0..lens[b].  With beta [H], M [B,Hkv,d,d] and z [B,Hkv,d] (fp32; all or none) the memory is
+    read and gated in as in the forward.  With weights, every row's softmax weight is added to
+    it.  lens < 0 marks a padding entry: its output is 0.  Returns out [B,H,d].
+    """
+    if q.dim() != 3:
+        raise ValueError("q is [B, H, d]")
+    dev = q.device
+    with _Launch(dev, stream) as handle:
+        P, Hkv, page, d = _pool(k_pages, v_pages, weights, dev)
+        B, max_pages = _table(page_table, lens, dev)
+        H, dt = q.shape[1], k_pages.dtype
+        _check(q, "q", dt, (B, H, d), dev)
+        _check(k, "k", dt, (B, Hkv, d), dev)
+        _check(v, "v", dt, (B, Hkv, d), dev)
+        _check(beta, "beta", torch.float32, (H,), dev)
+        _check(M, "M", torch.float32, (B, Hkv, d, d), dev)
+        _check(z, "z", torch.float32, (B, Hkv, d), dev)
+        _check(positions, "positions", torch.int64, (B,), dev)
+        rot = 0
+        if freq is not None:
+            rot = 2 * freq.numel()
+            _check(freq, "freq", torch.float64, (rot // 2,), dev)
+        elif positions is not None:
+            raise ValueError("positions without freq")
+        if out is None:
+            out = torch.empty((B, H, d), dtype=dt, device=dev)
+        _check(out, "out", dt, (B, H, d), dev)
+        need = LIB.infini_attn_paged_decode_workspace_bytes(B, H, Hkv, d, P, page,
+                                                            0 if weights is None else 1)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        _run(_entry("infini_attn_paged_decode_step", dt), _ptr(q), _ptr(k), _ptr(v),
+             _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(lens), _ptr(beta), _ptr(M),
+             _ptr(z), _ptr(weights), _ptr(freq), _ptr(positions), _ptr(out), _ptr(ws), need, B, H,
+             Hkv, d, P, page, max_pages, rot, 1 if interleaved else 0, float(scale), handle)
+    return out
+
+
+def paged_evict(k_pages, v_pages, weights, page_table, lens, dst_table, *, budget: int,
+                recent: int = 0, M=None, z=None, rule="linear", lens_out=None, kept=None,
+                stream=None):
+    """Cut every sequence to ``budget`` rows: the last ``recent`` ones and, of the others, those
+    of the highest accumulated weight (per key/value head; ties keep the lowest row).  The kept
+    rows are copied, in order, to the pages dst_table [B,dst_pages] int32 names, which must be
+    pages of their own.  With M [B,Hkv,d,d] and z [B,Hkv,d] the evicted rows are folded into the
+    memory in place.  Returns (lens_out [B], kept [B,Hkv,budget] int32: old rows, -1 padded).
+    """
+    dev = k_pages.device
+    with _Launch(dev, stream) as handle:
+        P, Hkv, page, d = _pool(k_pages, v_pages, weights, dev)
+        if weights is None:
+            raise ValueError("eviction needs the accumulated weights")
+        B, max_pages = _table(page_table, lens, dev)
+        Bd, dst_pages = _table(dst_table, lens, dev, "dst_table")
+        budget = int(budget)
+        _check(M, "M", torch.float32, (B, Hkv, d, d), dev)
+        _check(z, "z", torch.float32, (B, Hkv, d), dev)
+        if lens_out is None:
+            lens_out = torch.empty((B,), dtype=torch.int32, device=dev)
+        if kept is None:
+            kept = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device=dev)
+        _check(lens_out, "lens_out", torch.int32, (B,), dev)
+        _check(kept, "kept", torch.int32, (B, Hkv, budget), dev)
+        need = LIB.infini_attn_paged_evict_workspace_bytes(B, Hkv, d, page, max_pages, budget,
+                                                           0 if M is None else 1)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        _run(_entry("infini_attn_paged_evict", k_pages.dtype), _ptr(k_pages), _ptr(v_pages),
+             _ptr(weights), _ptr(page_table), _ptr(lens), _ptr(dst_table), _ptr(lens_out),
+             _ptr(kept), _ptr(M), _ptr(z), _ptr(ws), need, B, Hkv, d, P, page, max_pages,
+             dst_pages, budget, int(recent), RULES[rule], handle)
+    return lens_out, kept

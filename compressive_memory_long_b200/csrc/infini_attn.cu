@@ -10,9 +10,11 @@
 #include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <new>
 #include <string>
 #include <vector>
 
+#include "host.h"
 #include "infini_attn.h"
 #include "simt_kernels.cuh"
 #include "tc_segment.cuh"
@@ -1365,6 +1367,14 @@ int backward(const void *q, const void *k, const void *v, const float *beta, con
 }
 
 }  // namespace
+
+TraceScope::TraceScope(const char *name, cudaStream_t st)
+{
+    if (trace::enabled.load() != 0) rec_ = new (std::nothrow) trace::Scope(name, st);
+}
+
+TraceScope::~TraceScope() { delete static_cast<trace::Scope *>(rec_); }
+
 }  // namespace infini
 
 extern "C" {
@@ -1480,6 +1490,7 @@ const char *infini_attn_status_string(int status)
     case INFINI_ERR_CUDA: return "CUDA error";
     case INFINI_ERR_OOM: return "workspace allocation failed";
     case INFINI_ERR_TIMEOUT: return "bounded device wait timed out";
+    case INFINI_ERR_PAGE: return "page number or row outside the paged cache";
     default: return "unknown status";
     }
 }
@@ -1493,7 +1504,10 @@ int infini_attn_device_status(infini_stream_t stream)
     int v = 0;
     if (cudaMemcpyFromSymbol(&v, infini::tc::g_wait_status, sizeof(int)) != cudaSuccess)
         return INFINI_ERR_CUDA;
-    if (v == 0) return INFINI_OK;
+    if (v == 0) {
+        const int pages = infini::take_page_status();
+        return pages < 0 ? INFINI_ERR_CUDA : pages > 0 ? INFINI_ERR_PAGE : INFINI_OK;
+    }
     const int zero = 0;
     cudaMemcpyToSymbol(infini::tc::g_wait_status, &zero, sizeof(int));
     return INFINI_ERR_TIMEOUT;

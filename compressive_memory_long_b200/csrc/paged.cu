@@ -1,0 +1,401 @@
+// Host side of the paged serving entry points: rotary positions, filling the paged cache,
+// one new token's attention over it, and eviction from it.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <initializer_list>
+
+#include "evict.cuh"
+#include "host.h"
+#include "infini_attn.h"
+#include "paged.cuh"
+#include "rotary.cuh"
+
+namespace infini {
+
+int take_page_status()
+{
+    int v = 0;
+    const int zero = 0;
+    if (cudaMemcpyFromSymbol(&v, paged::g_page_status, sizeof(int)) != cudaSuccess) return -1;
+    if (v != 0 && cudaMemcpyToSymbol(paged::g_page_status, &zero, sizeof(int)) != cudaSuccess) return -1;
+    return v != 0;
+}
+
+namespace {
+
+using namespace paged;
+
+bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+struct Range {
+    const void *p;
+    int64_t bytes;
+    bool written;
+};
+
+// Whether some written range overlaps another one (empty and null ranges overlap nothing).
+bool clash(std::initializer_list<Range> rs)
+{
+    for (const Range *x = rs.begin(); x != rs.end(); ++x)
+        for (const Range *y = x + 1; y != rs.end(); ++y) {
+            if (!(x->written || y->written) || !x->p || !y->p || x->bytes <= 0 || y->bytes <= 0)
+                continue;
+            const uintptr_t x0 = (uintptr_t)x->p, y0 = (uintptr_t)y->p;
+            if (x0 < y0 + (uintptr_t)y->bytes && y0 < x0 + (uintptr_t)x->bytes) return true;
+        }
+    return false;
+}
+
+bool head_dim(int64_t d) { return d == 32 || d == 64 || d == 128; }
+
+// Strides (batch, head, token) of a [B, H, L, d] input: contiguous when none are given.
+bool take_strides(const int64_t *given, int64_t H, int64_t L, int64_t d, int64_t out[3])
+{
+    out[0] = H * L * d;
+    out[1] = L * d;
+    out[2] = d;
+    if (!given) return true;
+    for (int i = 0; i < 3; ++i) {
+        if (given[i] < 0 || given[i] > ((int64_t)1 << 42)) return false;
+        out[i] = given[i];
+    }
+    return true;
+}
+
+int64_t extent_bytes(const int64_t s[3], int64_t B, int64_t H, int64_t L, int64_t d, int64_t es)
+{
+    return ((B - 1) * s[0] + (H - 1) * s[1] + (L - 1) * s[2] + d) * es;
+}
+
+int launched(cudaError_t e = cudaGetLastError()) { return e == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA; }
+
+// ---- rotary positions ---------------------------------------------------------------------
+
+template <typename T>
+int rotary(const void *q, const void *k, void *q_out, void *k_out, const double *freq,
+           const int64_t *positions, int64_t start, const int64_t *q_strides,
+           const int64_t *k_strides, int64_t B, int64_t H, int64_t Hkv, int64_t L, int64_t d,
+           int64_t rot, int interleaved, float scale, int backward, infini_stream_t stream)
+{
+    if (!q || !q_out || (k == nullptr) != (k_out == nullptr)) return INFINI_ERR_INVALID_ARG;
+    if (B <= 0 || H <= 0 || L <= 0 || d <= 0 || (k && Hkv <= 0)) return INFINI_ERR_INVALID_ARG;
+    if (rot < 0 || rot > d || rot % 2 != 0 || (rot > 0 && !freq)) return INFINI_ERR_INVALID_ARG;
+    if (!k) Hkv = 0;
+    if (B > (1 << 20) || H > (1 << 16) || Hkv > (1 << 16) || L > ((int64_t)1 << 34) ||
+        B * L > ((int64_t)1 << 34) || B * (H + Hkv) * L > ((int64_t)1 << 40))
+        return INFINI_ERR_INVALID_ARG;
+    const int64_t es = (int64_t)sizeof(T);
+    RotaryArgs a{};
+    if (!take_strides(q_strides, H, L, d, a.sq) || !take_strides(k_strides, Hkv, L, d, a.sk))
+        return INFINI_ERR_INVALID_ARG;
+    if (!aligned(q, es) || !aligned(k, es) || !aligned(q_out, 16) || !aligned(k_out, 16) ||
+        !aligned(freq, 16) || !aligned(positions, 16))
+        return INFINI_ERR_INVALID_ARG;
+    const int64_t qb = B * H * L * d * es, kb = B * Hkv * L * d * es;
+    const int64_t qx = extent_bytes(a.sq, B, H, L, d, es), kx = k ? extent_bytes(a.sk, B, Hkv, L, d, es) : 0;
+    int64_t cq[3], ck[3];
+    take_strides(nullptr, H, L, d, cq);
+    take_strides(nullptr, Hkv, L, d, ck);
+    auto same = [](const int64_t *x, const int64_t *y) { return x[0] == y[0] && x[1] == y[1] && x[2] == y[2]; };
+    // in place: a contiguous input that is its own output
+    const bool q_in = q == q_out && same(a.sq, cq), k_in = k && k == k_out && same(a.sk, ck);
+    if (clash({{q_out, qb, true}, {k_out, kb, true}, {q_in ? nullptr : q, qx, false},
+               {k_in ? nullptr : k, kx, false}, {freq, rot / 2 * 8, false},
+               {positions, B * L * 8, false}}))
+        return INFINI_ERR_INVALID_ARG;
+    if (!head_dim(d)) return INFINI_ERR_UNSUPPORTED;
+    a.freq = freq;
+    a.positions = positions;
+    a.start = start;
+    a.L = L;
+    a.H = (int)H;
+    a.Hkv = (int)Hkv;
+    a.rot = (int)rot;
+    a.interleaved = interleaved != 0;
+    a.backward = backward;
+    a.scale = scale;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaGetLastError();
+    const T *tq = static_cast<const T *>(q), *tk = static_cast<const T *>(k);
+    T *oq = static_cast<T *>(q_out), *ok = static_cast<T *>(k_out);
+    TraceScope trace("rotary", st);
+    const int64_t n = B * L * (d / 2);
+    const unsigned grid = (unsigned)((n + 255) / 256);
+    switch (d) {
+    case 32: k_rotary<T, 32><<<grid, 256, 0, st>>>(tq, tk, oq, ok, a, n); break;
+    case 64: k_rotary<T, 64><<<grid, 256, 0, st>>>(tq, tk, oq, ok, a, n); break;
+    default: k_rotary<T, 128><<<grid, 256, 0, st>>>(tq, tk, oq, ok, a, n); break;
+    }
+    return launched();
+}
+
+// ---- the paged cache ------------------------------------------------------------------------
+
+// Sizes of a paged cache; `shift` with page = 1 << shift.
+int check_pool(int64_t B, int64_t Hkv, int64_t P, int64_t page, int64_t max_pages, int *shift)
+{
+    if (B <= 0 || Hkv <= 0 || P <= 0 || page <= 0 || max_pages <= 0) return INFINI_ERR_INVALID_ARG;
+    if (B > (1 << 20) || Hkv > (1 << 16) || B * Hkv > ((int64_t)1 << 24) || P > ((int64_t)1 << 31) - 1 ||
+        page > (1 << 20) || max_pages > ((int64_t)1 << 31) - 1 || max_pages * page > ((int64_t)1 << 30) ||
+        B * max_pages > ((int64_t)1 << 40) || P * page * Hkv > ((int64_t)1 << 40))
+        return INFINI_ERR_INVALID_ARG;
+    if ((page & (page - 1)) != 0) return INFINI_ERR_UNSUPPORTED;
+    *shift = 0;
+    while (((int64_t)1 << *shift) < page) ++*shift;
+    return INFINI_OK;
+}
+
+template <typename T>
+int paged_append(const void *k, const void *v, const int64_t *k_strides, const int64_t *v_strides,
+                 void *k_pages, void *v_pages, float *weights, const int *table, const int *lens,
+                 const int *counts, int64_t B, int64_t Hkv, int64_t Tn, int64_t d, int64_t P,
+                 int64_t page, int64_t max_pages, infini_stream_t stream)
+{
+    if (!k || !v || !k_pages || !v_pages || !table || !lens || Tn <= 0 || d <= 0)
+        return INFINI_ERR_INVALID_ARG;
+    PageArgs a{table, lens, P, (int)max_pages, 0, (int)Hkv};
+    const int rc = check_pool(B, Hkv, P, page, max_pages, &a.shift);
+    if (rc == INFINI_ERR_INVALID_ARG) return rc;
+    if (Tn > ((int64_t)1 << 30) || B * Hkv * Tn > ((int64_t)1 << 32)) return INFINI_ERR_INVALID_ARG;
+    const int64_t es = (int64_t)sizeof(T), pool = P * Hkv * page;
+    int64_t sk[3], sv[3];
+    if (!take_strides(k_strides, Hkv, Tn, d, sk) || !take_strides(v_strides, Hkv, Tn, d, sv))
+        return INFINI_ERR_INVALID_ARG;
+    if (!aligned(k, es) || !aligned(v, es) || !aligned(k_pages, 16) || !aligned(v_pages, 16) ||
+        !aligned(weights, 16) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(counts, 4))
+        return INFINI_ERR_INVALID_ARG;
+    if (clash({{k_pages, pool * d * es, true}, {v_pages, pool * d * es, true}, {weights, pool * 4, true},
+               {k, extent_bytes(sk, B, Hkv, Tn, d, es), false},
+               {v, extent_bytes(sv, B, Hkv, Tn, d, es), false}, {table, B * max_pages * 4, false},
+               {lens, B * 4, false}, {counts, B * 4, false}}))
+        return INFINI_ERR_INVALID_ARG;
+    if (rc != INFINI_OK || !head_dim(d)) return INFINI_ERR_UNSUPPORTED;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaGetLastError();
+    const T *tk = static_cast<const T *>(k), *tv = static_cast<const T *>(v);
+    T *kp = static_cast<T *>(k_pages), *vp = static_cast<T *>(v_pages);
+    TraceScope trace("paged_append", st);
+    const int64_t n = B * Hkv * Tn * d;
+    const unsigned grid = (unsigned)((n + 255) / 256);
+#define APPEND(D)                                                                                  \
+    k_paged_append<T, D><<<grid, 256, 0, st>>>(tk, tv, kp, vp, weights, a, counts, sk[0], sk[1], sk[2], \
+                                               sv[0], sv[1], sv[2], Tn, n)
+    switch (d) {
+    case 32: APPEND(32); break;
+    case 64: APPEND(64); break;
+    default: APPEND(128); break;
+    }
+#undef APPEND
+    return launched();
+}
+
+int64_t decode_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int) { return 0; }
+
+template <typename T>
+int paged_decode_step(const void *q, const void *k, const void *v, void *k_pages, void *v_pages,
+                      const int *table, const int *lens, const float *beta, const float *M,
+                      const float *z, float *weights, const double *freq, const int64_t *positions,
+                      void *out, void *workspace, int64_t workspace_bytes, int64_t B, int64_t H,
+                      int64_t Hkv, int64_t d, int64_t P, int64_t page, int64_t max_pages,
+                      int64_t rot, int interleaved, float scale, infini_stream_t stream)
+{
+    if (!q || !k_pages || !v_pages || !table || !lens || !out || (k == nullptr) != (v == nullptr))
+        return INFINI_ERR_INVALID_ARG;
+    if ((beta == nullptr) != (M == nullptr) || (beta == nullptr) != (z == nullptr))
+        return INFINI_ERR_INVALID_ARG;
+    PageArgs a{table, lens, P, (int)max_pages, 0, (int)Hkv};
+    const int rc = check_pool(B, Hkv, P, page, max_pages, &a.shift);
+    if (rc == INFINI_ERR_INVALID_ARG) return rc;
+    if (H <= 0 || H % Hkv != 0 || H > (1 << 16) || B * H > ((int64_t)1 << 31) - 1 || d <= 0 || rot < 0 ||
+        rot > d || rot % 2 != 0 || (rot > 0 && !freq))
+        return INFINI_ERR_INVALID_ARG;
+    const int64_t need = decode_workspace_bytes(B, H, Hkv, d, P, page, weights != nullptr);
+    if (workspace_bytes < need || (need > 0 && !workspace)) return INFINI_ERR_INVALID_ARG;
+    for (const void *p : {q, k, v, (const void *)k_pages, (const void *)v_pages, (const void *)beta,
+                          (const void *)M, (const void *)z, (const void *)weights, (const void *)freq,
+                          (const void *)positions, (const void *)out, (const void *)workspace})
+        if (!aligned(p, 16)) return INFINI_ERR_INVALID_ARG;
+    if (!aligned(table, 4) || !aligned(lens, 4)) return INFINI_ERR_INVALID_ARG;
+    const int64_t es = (int64_t)sizeof(T), pool = P * Hkv * page;
+    if (clash({{k_pages, pool * d * es, true}, {v_pages, pool * d * es, true}, {weights, pool * 4, true},
+               {out, B * H * d * es, true}, {workspace, need, true}, {q, B * H * d * es, false},
+               {k, B * Hkv * d * es, false}, {v, B * Hkv * d * es, false},
+               {table, B * max_pages * 4, false}, {lens, B * 4, false}, {beta, H * 4, false},
+               {M, B * Hkv * d * d * 4, false}, {z, B * Hkv * d * 4, false}, {freq, rot / 2 * 8, false},
+               {positions, B * 8, false}}))
+        return INFINI_ERR_INVALID_ARG;
+    if (rc != INFINI_OK || !head_dim(d)) return INFINI_ERR_UNSUPPORTED;
+    const DecodeArgs dc{beta, M, z, rot > 0 ? freq : nullptr, positions, (int)H, (int)rot,
+                        interleaved != 0, scale};
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaGetLastError();
+    const T *tq = static_cast<const T *>(q), *tk = static_cast<const T *>(k), *tv = static_cast<const T *>(v);
+    T *kp = static_cast<T *>(k_pages), *vp = static_cast<T *>(v_pages), *to = static_cast<T *>(out);
+    TraceScope trace("paged_decode", st);
+    const unsigned grid = (unsigned)(B * Hkv);
+    switch (d) {
+    case 32: k_paged_decode<T, 32><<<grid, 256, 0, st>>>(tq, tk, tv, kp, vp, weights, to, a, dc); break;
+    case 64: k_paged_decode<T, 64><<<grid, 256, 0, st>>>(tq, tk, tv, kp, vp, weights, to, a, dc); break;
+    default: k_paged_decode<T, 128><<<grid, 256, 0, st>>>(tq, tk, tv, kp, vp, weights, to, a, dc); break;
+    }
+    return launched();
+}
+
+// The evicted rows of every (batch, kv head), when they go into a memory.
+int64_t evict_workspace_bytes(int64_t B, int64_t Hkv, int64_t page, int64_t max_pages, int64_t budget,
+                              int with_memory)
+{
+    const int64_t most = max_pages * page - budget;
+    return with_memory && most > 0 ? B * Hkv * most * 4 : 0;
+}
+
+template <typename T, int D>
+int launch_evict(T *kp, T *vp, float *weights, const PageArgs &a, const EvictArgs &e, float *M, float *z,
+                 int64_t units, cudaStream_t st)
+{
+    {
+        TraceScope trace("evict_select", st);
+        k_evict_select<<<(unsigned)units, 1024, 0, st>>>(weights, a, e);
+    }
+    if (M && e.gone) {
+        TraceScope trace("evict_fold", st);
+        k_evict_fold<T, D><<<(unsigned)units, 256, 0, st>>>(kp, vp, a, e, M, z);
+    }
+    TraceScope trace("evict_move", st);
+    k_evict_move<T, D><<<(unsigned)((units * e.budget + 7) / 8), 256, 0, st>>>(kp, vp, weights, a, e,
+                                                                                  units * e.budget);
+    return launched();
+}
+
+template <typename T>
+int paged_evict(void *k_pages, void *v_pages, float *weights, const int *table, const int *lens,
+                const int *dst_table, int *lens_out, int *kept, float *M, float *z, void *workspace,
+                int64_t workspace_bytes, int64_t B, int64_t Hkv, int64_t d, int64_t P, int64_t page,
+                int64_t max_pages, int64_t dst_pages, int64_t budget, int64_t recent, int rule,
+                infini_stream_t stream)
+{
+    if (!k_pages || !v_pages || !weights || !table || !lens || !dst_table || !lens_out || !kept ||
+        (M == nullptr) != (z == nullptr))
+        return INFINI_ERR_INVALID_ARG;
+    if (rule != INFINI_UPDATE_LINEAR && rule != INFINI_UPDATE_DELTA) return INFINI_ERR_INVALID_ARG;
+    PageArgs a{table, lens, P, (int)max_pages, 0, (int)Hkv};
+    int rc = check_pool(B, Hkv, P, page, max_pages, &a.shift);
+    if (rc == INFINI_ERR_INVALID_ARG) return rc;
+    if (d <= 0 || budget <= 0 || recent < 0 || recent > budget || dst_pages <= 0 ||
+        dst_pages > ((int64_t)1 << 31) - 1 || dst_pages * page < budget ||
+        B * Hkv * budget > ((int64_t)1 << 33))
+        return INFINI_ERR_INVALID_ARG;
+    const int64_t es = (int64_t)sizeof(T), pool = P * Hkv * page, units = B * Hkv;
+    const int64_t need = evict_workspace_bytes(B, Hkv, page, max_pages, budget, M != nullptr);
+    if (workspace_bytes < need || (need > 0 && !workspace)) return INFINI_ERR_INVALID_ARG;
+    for (const void *p : {(const void *)k_pages, (const void *)v_pages, (const void *)weights,
+                          (const void *)M, (const void *)z, (const void *)workspace, (const void *)kept})
+        if (!aligned(p, 16)) return INFINI_ERR_INVALID_ARG;
+    for (const int *p : {table, lens, dst_table, (const int *)lens_out})
+        if (!aligned(p, 4)) return INFINI_ERR_INVALID_ARG;
+    // lens_out may be lens itself
+    if (clash({{k_pages, pool * d * es, true}, {v_pages, pool * d * es, true}, {weights, pool * 4, true},
+               {lens_out, B * 4, true}, {kept, units * budget * 4, true}, {M, units * d * d * 4, true},
+               {z, units * d * 4, true}, {workspace, need, true}, {table, B * max_pages * 4, false},
+               {lens, B * 4, false}, {dst_table, B * dst_pages * 4, false}}))
+        return INFINI_ERR_INVALID_ARG;
+    if (rc != INFINI_OK || !head_dim(d)) return INFINI_ERR_UNSUPPORTED;
+    if (M && rule == INFINI_UPDATE_DELTA) return INFINI_ERR_UNSUPPORTED;
+    const EvictArgs e{dst_table, (int)dst_pages, (int)budget, (int)recent, lens_out, kept,
+                      need > 0 ? static_cast<int *>(workspace) : nullptr, max_pages * page - budget};
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaGetLastError();
+    T *kp = static_cast<T *>(k_pages), *vp = static_cast<T *>(v_pages);
+    switch (d) {
+    case 32: return launch_evict<T, 32>(kp, vp, weights, a, e, M, z, units, st);
+    case 64: return launch_evict<T, 64>(kp, vp, weights, a, e, M, z, units, st);
+    default: return launch_evict<T, 128>(kp, vp, weights, a, e, M, z, units, st);
+    }
+}
+
+}  // namespace
+}  // namespace infini
+
+using bf16 = __nv_bfloat16;
+
+extern "C" {
+
+#define ROTARY_ENTRY(name, T, backward)                                                            \
+    int name(const void *q, const void *k, void *q_out, void *k_out, const double *freq,           \
+             const int64_t *positions, int64_t start, const int64_t *q_strides,                    \
+             const int64_t *k_strides, int64_t B, int64_t H, int64_t Hkv, int64_t L, int64_t d,    \
+             int64_t rot, int interleaved, float scale, infini_stream_t stream)                    \
+    {                                                                                              \
+        return infini::rotary<T>(q, k, q_out, k_out, freq, positions, start, q_strides, k_strides, \
+                                 B, H, Hkv, L, d, rot, interleaved, scale, backward, stream);      \
+    }
+ROTARY_ENTRY(infini_attn_rotary, bf16, 0)
+ROTARY_ENTRY(infini_attn_rotary_f32, float, 0)
+ROTARY_ENTRY(infini_attn_rotary_bwd, bf16, 1)
+ROTARY_ENTRY(infini_attn_rotary_bwd_f32, float, 1)
+#undef ROTARY_ENTRY
+
+#define APPEND_ENTRY(name, T)                                                                      \
+    int name(const void *k, const void *v, const int64_t *k_strides, const int64_t *v_strides,     \
+             void *k_pages, void *v_pages, float *weights, const int32_t *page_table,              \
+             const int32_t *lens, const int32_t *counts, int64_t B, int64_t Hkv, int64_t T_new,    \
+             int64_t d, int64_t P, int64_t page, int64_t max_pages, infini_stream_t stream)        \
+    {                                                                                              \
+        return infini::paged_append<T>(k, v, k_strides, v_strides, k_pages, v_pages, weights,      \
+                                       page_table, lens, counts, B, Hkv, T_new, d, P, page,        \
+                                       max_pages, stream);                                         \
+    }
+APPEND_ENTRY(infini_attn_paged_append, bf16)
+APPEND_ENTRY(infini_attn_paged_append_f32, float)
+#undef APPEND_ENTRY
+
+#define DECODE_ENTRY(name, T)                                                                      \
+    int name(const void *q, const void *k, const void *v, void *k_pages, void *v_pages,            \
+             const int32_t *page_table, const int32_t *lens, const float *beta, const float *M,    \
+             const float *z, float *weights, const double *freq, const int64_t *positions,         \
+             void *out, void *workspace, int64_t workspace_bytes, int64_t B, int64_t H,            \
+             int64_t Hkv, int64_t d, int64_t P, int64_t page, int64_t max_pages, int64_t rot,      \
+             int interleaved, float scale, infini_stream_t stream)                                 \
+    {                                                                                              \
+        return infini::paged_decode_step<T>(q, k, v, k_pages, v_pages, page_table, lens, beta, M,  \
+                                            z, weights, freq, positions, out, workspace,           \
+                                            workspace_bytes, B, H, Hkv, d, P, page, max_pages,     \
+                                            rot, interleaved, scale, stream);                      \
+    }
+DECODE_ENTRY(infini_attn_paged_decode_step, bf16)
+DECODE_ENTRY(infini_attn_paged_decode_step_f32, float)
+#undef DECODE_ENTRY
+
+#define EVICT_ENTRY(name, T)                                                                       \
+    int name(void *k_pages, void *v_pages, float *weights, const int32_t *page_table,              \
+             const int32_t *lens, const int32_t *dst_table, int32_t *lens_out, int32_t *kept,      \
+             float *M, float *z, void *workspace, int64_t workspace_bytes, int64_t B, int64_t Hkv, \
+             int64_t d, int64_t P, int64_t page, int64_t max_pages, int64_t dst_pages,             \
+             int64_t budget, int64_t recent, int update_rule, infini_stream_t stream)              \
+    {                                                                                              \
+        return infini::paged_evict<T>(k_pages, v_pages, weights, page_table, lens, dst_table,      \
+                                      lens_out, kept, M, z, workspace, workspace_bytes, B, Hkv, d, \
+                                      P, page, max_pages, dst_pages, budget, recent, update_rule,  \
+                                      stream);                                                     \
+    }
+EVICT_ENTRY(infini_attn_paged_evict, bf16)
+EVICT_ENTRY(infini_attn_paged_evict_f32, float)
+#undef EVICT_ENTRY
+
+int64_t infini_attn_paged_decode_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t d, int64_t P,
+                                                 int64_t page, int with_weights)
+{
+    if (B <= 0 || Hkv <= 0 || H <= 0 || d <= 0 || P <= 0 || page <= 0) return 0;
+    return infini::decode_workspace_bytes(B, H, Hkv, d, P, page, with_weights);
+}
+
+int64_t infini_attn_paged_evict_workspace_bytes(int64_t B, int64_t Hkv, int64_t d, int64_t page,
+                                                int64_t max_pages, int64_t budget, int with_memory)
+{
+    if (B <= 0 || Hkv <= 0 || d <= 0 || page <= 0 || max_pages <= 0 || budget <= 0) return 0;
+    return infini::evict_workspace_bytes(B, Hkv, page, max_pages, budget, with_memory);
+}
+
+}  // extern "C"

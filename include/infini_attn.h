@@ -72,7 +72,9 @@ enum {
     INFINI_ERR_UNSUPPORTED = 2, /* valid but not built: d not in {32, 64, 128}, N % 64 != 0 */
     INFINI_ERR_CUDA = 3,        /* a CUDA runtime call or launch failed                      */
     INFINI_ERR_OOM = 4,         /* the workspace allocation failed                           */
-    INFINI_ERR_TIMEOUT = 5      /* a bounded device wait gave up (infini_attn_device_status) */
+    INFINI_ERR_TIMEOUT = 5,     /* a bounded device wait gave up (infini_attn_device_status) */
+    INFINI_ERR_PAGE = 6         /* a kernel met a page number or row outside the paged cache
+                                   (infini_attn_device_status)                             */
 };
 
 /*
@@ -193,6 +195,154 @@ INFINI_API int infini_attn_fold_f32(const void *k_cache, const void *v_cache, in
                                     int64_t d, int update_rule, infini_stream_t stream);
 
 /*
+ * Rotary positions.  The first `rot` channels of every head of q and k are turned in pairs by
+ * the angle position * freq[i], i < rot / 2, and scaled:
+ *     y1 = scale (x1 cos a - x2 sin a),   y2 = scale (x2 cos a + x1 sin a)
+ * Pair i is channels (i, i + rot / 2), or (2 i, 2 i + 1) when `interleaved`; channels >= rot are
+ * copied.  Apply it before infini_attn_fwd: the forward takes rotated q and k.  Angles are
+ * formed and reduced in 64 bits, so positions far into a stream keep their fraction.
+ *
+ *   q [B, H, L, d], k [B, Hkv, L, d]: read through q_strides / k_strides, three element
+ *     strides (batch, head, token) in HOST memory; NULL = contiguous.  The last dimension is
+ *     contiguous; element alignment suffices (16-byte aligned rows are faster).  k may be NULL
+ *     (with k_out): q alone.
+ *   q_out, k_out: contiguous; each may be its own (contiguous) input
+ *   freq [rot / 2] double (rot even, 0 <= rot <= d);  positions [B, L] int64, or NULL: token t
+ *     is at start + t.  Negative positions are valid.
+ * The _bwd entries map the gradients of q_out, k_out to those of q, k with the same arguments
+ * (the angle negated); they take the gradients in the place of q, k.
+ */
+INFINI_API int infini_attn_rotary(const void *q, const void *k, void *q_out, void *k_out,
+                                  const double *freq, const int64_t *positions, int64_t start,
+                                  const int64_t *q_strides, const int64_t *k_strides, int64_t B,
+                                  int64_t H, int64_t Hkv, int64_t L, int64_t d, int64_t rot,
+                                  int interleaved, float scale, infini_stream_t stream);
+INFINI_API int infini_attn_rotary_f32(const void *q, const void *k, void *q_out, void *k_out,
+                                      const double *freq, const int64_t *positions, int64_t start,
+                                      const int64_t *q_strides, const int64_t *k_strides, int64_t B,
+                                      int64_t H, int64_t Hkv, int64_t L, int64_t d, int64_t rot,
+                                      int interleaved, float scale, infini_stream_t stream);
+INFINI_API int infini_attn_rotary_bwd(const void *dq_out, const void *dk_out, void *dq, void *dk,
+                                      const double *freq, const int64_t *positions, int64_t start,
+                                      const int64_t *q_strides, const int64_t *k_strides, int64_t B,
+                                      int64_t H, int64_t Hkv, int64_t L, int64_t d, int64_t rot,
+                                      int interleaved, float scale, infini_stream_t stream);
+INFINI_API int infini_attn_rotary_bwd_f32(const void *dq_out, const void *dk_out, void *dq, void *dk,
+                                          const double *freq, const int64_t *positions, int64_t start,
+                                          const int64_t *q_strides, const int64_t *k_strides,
+                                          int64_t B, int64_t H, int64_t Hkv, int64_t L, int64_t d,
+                                          int64_t rot, int interleaved, float scale,
+                                          infini_stream_t stream);
+
+/*
+ * Decode over a paged cache: a batch whose sequences are at different places.
+ *
+ *   k_pages, v_pages [P, Hkv, page, d] (activation dtype): a pool of P pages, `page` rows each
+ *     (a power of two; other sizes are INFINI_ERR_UNSUPPORTED)
+ *   page_table [B, max_pages] int32: row r of sequence b lies in page page_table[b][r / page],
+ *     slot r % page, the same for every key/value head.  Entries past a sequence's rows are not
+ *     read.  Sequences may share pages that no call writes.
+ *   lens [B] int32: rows each sequence has in the cache; negative: a padding entry of the
+ *     batch, which reads and writes no page.  Calls do not change lens (all layers of a model
+ *     share it): the caller adds the rows it appended.
+ *   weights [P, Hkv, page] float: per row, the softmax weight it has received so far, summed
+ *     over the group's query heads and the steps (NULL: not kept)
+ * No entry allocates memory; all may be captured in a graph.  A workspace, where one is asked
+ * for, holds nothing between calls, and calls that may overlap on the GPU need one each.
+ * page_table and lens are read on the device: a page number outside [0, P), or a row past the
+ * table's end, is never followed.  Such a row is left out (not read, not written), and
+ * infini_attn_device_status reports INFINI_ERR_PAGE.
+ * page_table, lens, counts, dst_table and lens_out need 4-byte alignment, the strided k and v
+ * of infini_attn_paged_append that of an element.
+ *
+ * infini_attn_paged_append: rows lens[b] .. lens[b] + counts[b] - 1 become the first counts[b]
+ * tokens of k, v [B, Hkv, T, d] (strides as for infini_attn_rotary; counts [B] int32, NULL: T
+ * for every sequence; a count beyond T counts as T), and their weights 0.
+ */
+INFINI_API int infini_attn_paged_append(const void *k, const void *v, const int64_t *k_strides,
+                                        const int64_t *v_strides, void *k_pages, void *v_pages,
+                                        float *weights, const int32_t *page_table,
+                                        const int32_t *lens, const int32_t *counts, int64_t B,
+                                        int64_t Hkv, int64_t T, int64_t d, int64_t P, int64_t page,
+                                        int64_t max_pages, infini_stream_t stream);
+INFINI_API int infini_attn_paged_append_f32(const void *k, const void *v, const int64_t *k_strides,
+                                            const int64_t *v_strides, void *k_pages, void *v_pages,
+                                            float *weights, const int32_t *page_table,
+                                            const int32_t *lens, const int32_t *counts, int64_t B,
+                                            int64_t Hkv, int64_t T, int64_t d, int64_t P,
+                                            int64_t page, int64_t max_pages,
+                                            infini_stream_t stream);
+
+/*
+ * infini_attn_paged_decode_step: one new token of every sequence, the counterpart of
+ * infini_attn_decode_step with a row count per sequence:
+ *   - rot > 0: q and k are rotated first, as by infini_attn_rotary, at positions [B] int64
+ *     (NULL: lens);
+ *   - k, v become row lens[b] (its weight starts at 0); with k = v = NULL nothing is appended
+ *     and the attention spans the cached rows alone;
+ *   - softmax attention of q over rows 0 .. lens[b]; a sequence without rows gives 0;
+ *   - with beta, M and z (all or none): the retrieval from (M, z) with the rotated q and the
+ *     gate, as in the forward; M and z are read only;
+ *   - with weights: every row's softmax weight, summed over the group's query heads, is added.
+ *     The pages of a sequence must then be its own.
+ * Padding entries (lens < 0) give rows of 0.
+ *   q [B, H, d], k / v [B, Hkv, d], out [B, H, d];  out and the workspace overlap nothing.
+ *   workspace: infini_attn_paged_decode_workspace_bytes(B, H, Hkv, d, P, page, weights != NULL)
+ */
+INFINI_API int infini_attn_paged_decode_step(
+    const void *q, const void *k, const void *v, void *k_pages, void *v_pages,
+    const int32_t *page_table, const int32_t *lens, const float *beta, const float *M,
+    const float *z, float *weights, const double *freq, const int64_t *positions, void *out,
+    void *workspace, int64_t workspace_bytes, int64_t B, int64_t H, int64_t Hkv, int64_t d,
+    int64_t P, int64_t page, int64_t max_pages, int64_t rot, int interleaved, float scale,
+    infini_stream_t stream);
+INFINI_API int infini_attn_paged_decode_step_f32(
+    const void *q, const void *k, const void *v, void *k_pages, void *v_pages,
+    const int32_t *page_table, const int32_t *lens, const float *beta, const float *M,
+    const float *z, float *weights, const double *freq, const int64_t *positions, void *out,
+    void *workspace, int64_t workspace_bytes, int64_t B, int64_t H, int64_t Hkv, int64_t d,
+    int64_t P, int64_t page, int64_t max_pages, int64_t rot, int interleaved, float scale,
+    infini_stream_t stream);
+INFINI_API int64_t infini_attn_paged_decode_workspace_bytes(int64_t B, int64_t H, int64_t Hkv,
+                                                            int64_t d, int64_t P, int64_t page,
+                                                            int with_weights);
+
+/*
+ * infini_attn_paged_evict: cut every sequence to `budget` rows.  Of its n = lens[b] rows every
+ * key/value head keeps the last `recent` (<= budget) and, of the others, those of the highest
+ * weights (ties: the lowest row; a NaN counts as the highest), min(n, budget) in all.  They are
+ * copied with their weights, in their old order, to rows 0, 1, ... of the pages dst_table
+ * [B, dst_pages] (dst_pages * page >= budget); every other row of the pool stays as it was.  The
+ * destination pages are written, so they must be in no other sequence and not among the pages of
+ * page_table; only a sequence of at most `budget` rows may name its own pages (in the same
+ * order), and nothing of it moves then.
+ *   lens_out [B]: min(lens[b], budget) (may not be lens itself)
+ *   kept [B, Hkv, budget] int32: the old rows of the kept ones, ascending, -1 past the last
+ *   M, z (both or none): the rows not kept are folded in, in place, as one update of the
+ *     forward's rule.  INFINI_UPDATE_DELTA is not built: INFINI_ERR_UNSUPPORTED.
+ *   workspace: infini_attn_paged_evict_workspace_bytes(B, Hkv, d, page, max_pages, budget,
+ *     M != NULL)
+ */
+INFINI_API int infini_attn_paged_evict(void *k_pages, void *v_pages, float *weights,
+                                       const int32_t *page_table, const int32_t *lens,
+                                       const int32_t *dst_table, int32_t *lens_out, int32_t *kept,
+                                       float *M, float *z, void *workspace, int64_t workspace_bytes,
+                                       int64_t B, int64_t Hkv, int64_t d, int64_t P, int64_t page,
+                                       int64_t max_pages, int64_t dst_pages, int64_t budget,
+                                       int64_t recent, int update_rule, infini_stream_t stream);
+INFINI_API int infini_attn_paged_evict_f32(void *k_pages, void *v_pages, float *weights,
+                                           const int32_t *page_table, const int32_t *lens,
+                                           const int32_t *dst_table, int32_t *lens_out,
+                                           int32_t *kept, float *M, float *z, void *workspace,
+                                           int64_t workspace_bytes, int64_t B, int64_t Hkv,
+                                           int64_t d, int64_t P, int64_t page, int64_t max_pages,
+                                           int64_t dst_pages, int64_t budget, int64_t recent,
+                                           int update_rule, infini_stream_t stream);
+INFINI_API int64_t infini_attn_paged_evict_workspace_bytes(int64_t B, int64_t Hkv, int64_t d,
+                                                           int64_t page, int64_t max_pages,
+                                                           int64_t budget, int with_memory);
+
+/*
  * Allocation-free variant of infini_attn_fwd (bf16 activations); same parameters, same
  * results.  The pages have no counterpart to this entry point: it exists for callers that
  * may not allocate device memory while they run, for example a serving loop whose device
@@ -235,6 +385,8 @@ INFINI_API int64_t infini_attn_workspace_bytes(int64_t B, int64_t Hkv, int64_t L
  * INFINI_OK, or INFINI_ERR_CUDA if the synchronisation itself failed.  A kernel whose wait
  * gave up stops early and leaves part of its outputs unwritten.  The record is sticky:
  * until it is read here, later launches of the waiting kernels return without work.
+ * INFINI_ERR_PAGE if instead a paged entry met a page number or row outside its cache since the
+ * last check (cleared too; later launches are not affected).
  */
 INFINI_API int infini_attn_device_status(infini_stream_t stream);
 
