@@ -4,12 +4,15 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+#include <atomic>
 #include <initializer_list>
 
 #include "evict.cuh"
 #include "host.h"
 #include "infini_attn.h"
 #include "paged.cuh"
+#include "paged_decode.cuh"
 #include "rotary.cuh"
 
 namespace infini {
@@ -70,6 +73,38 @@ int64_t extent_bytes(const int64_t s[3], int64_t B, int64_t H, int64_t L, int64_
 }
 
 int launched(cudaError_t e = cudaGetLastError()) { return e == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA; }
+
+// Lets `Kernel` use `bytes` of dynamic shared memory on the current device (asked once each).
+template <auto Kernel>
+bool opt_in_smem(size_t bytes)
+{
+    static std::atomic<uint64_t> done_mask{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev < 64 && (done_mask.load(std::memory_order_relaxed) & bit)) return true;
+    if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
+        return false;
+    done_mask.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
+
+// Launches a kernel that may start while the one before it on the stream still runs (it waits
+// for that one's end itself).
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t st, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
 
 // ---- rotary positions ---------------------------------------------------------------------
 
@@ -191,7 +226,51 @@ int paged_append(const void *k, const void *v, const int64_t *k_strides, const i
     return launched();
 }
 
-int64_t decode_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int) { return 0; }
+// Pieces' outputs and statistics, and with weights every cached row's scores.
+int64_t decode_slots(int64_t B, int64_t H, int64_t Hkv)
+{
+    return kSplitCtas + B * Hkv * ((H / Hkv + 7) / 8);
+}
+
+int64_t decode_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t d, int64_t P, int64_t page,
+                               int with_weights)
+{
+    const int64_t parts = decode_slots(B, H, Hkv) * std::min<int64_t>(H / Hkv, 8) * (d + 2);
+    return (parts + 3) / 4 * 16 + (with_weights ? P * page * H * 4 : 0);
+}
+
+template <typename T, int D, int GT>
+int launch_decode(const T *q, const T *k, const T *v, T *kp, T *vp, float *weights, T *out, const PageArgs &a,
+                  const DecodeArgs &dc, int64_t most_rows, cudaStream_t st)
+{
+    constexpr size_t smem = kSplitWarps * kStages * (8192 + DecodeTile<T, D>::R * 8) + 3 * GT * D * 4;
+    if (!opt_in_smem<k_paged_split<T, D, GT>>(smem)) return INFINI_ERR_CUDA;
+    {
+        TraceScope trace("paged_split", st);
+        k_paged_split<T, D, GT><<<kSplitCtas, 32 * kSplitWarps, smem, st>>>(q, k, v, kp, vp, a, dc);
+    }
+    const int rc = launched();
+    if (rc != INFINI_OK) return rc;
+    TraceScope trace("paged_join", st);
+    const int64_t units = dc.B * a.Hkv;
+    int64_t chunks = 1;
+    if (weights)   // enough CTAs for every SM several times over; a chunk takes more rows then
+        chunks = std::max<int64_t>(1, std::min((most_rows + kJoinRows - 1) / kJoinRows, 2368 / units));
+    return launched(launch_early(k_paged_join<T, D>, dim3((unsigned)units, (unsigned)chunks), kJoinThreads, st, q,
+                                 weights, out, a, dc, k ? 1 : 0));
+}
+
+template <typename T, int D>
+int pick_decode(const T *q, const T *k, const T *v, T *kp, T *vp, float *weights, T *out, const PageArgs &a,
+                const DecodeArgs &dc, int64_t most_rows, cudaStream_t st)
+{
+    if constexpr (sizeof(T) == 4) {   // as many heads at a time as there are
+        if (dc.hg == 1) return launch_decode<T, D, 1>(q, k, v, kp, vp, weights, out, a, dc, most_rows, st);
+        if (dc.hg == 2) return launch_decode<T, D, 2>(q, k, v, kp, vp, weights, out, a, dc, most_rows, st);
+        if (dc.hg <= 4) return launch_decode<T, D, 4>(q, k, v, kp, vp, weights, out, a, dc, most_rows, st);
+    }
+    return launch_decode<T, D, 8>(q, k, v, kp, vp, weights, out, a, dc, most_rows, st);
+}
 
 template <typename T>
 int paged_decode_step(const void *q, const void *k, const void *v, void *k_pages, void *v_pages,
@@ -227,20 +306,34 @@ int paged_decode_step(const void *q, const void *k, const void *v, void *k_pages
                {positions, B * 8, false}}))
         return INFINI_ERR_INVALID_ARG;
     if (rc != INFINI_OK || !head_dim(d)) return INFINI_ERR_UNSUPPORTED;
-    const DecodeArgs dc{beta, M, z, rot > 0 ? freq : nullptr, positions, (int)H, (int)rot,
-                        interleaved != 0, scale};
+    DecodeArgs dc{};
+    dc.beta = beta;
+    dc.M = M;
+    dc.z = z;
+    dc.freq = rot > 0 ? freq : nullptr;
+    dc.positions = positions;
+    dc.H = (int)H;
+    dc.rot = (int)rot;
+    dc.interleaved = interleaved != 0;
+    dc.rot_scale = scale;
+    dc.G = (int)(H / Hkv);
+    dc.HT = (dc.G + 7) / 8;
+    dc.hg = std::min(dc.G, 8);
+    dc.B = B;
+    const int64_t slots = decode_slots(B, H, Hkv);
+    dc.part_o = static_cast<float *>(workspace);
+    dc.part_ml = dc.part_o + slots * dc.hg * d;
+    dc.scores = weights ? dc.part_o + (slots * dc.hg * (d + 2) + 3) / 4 * 4 : nullptr;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaGetLastError();
     const T *tq = static_cast<const T *>(q), *tk = static_cast<const T *>(k), *tv = static_cast<const T *>(v);
     T *kp = static_cast<T *>(k_pages), *vp = static_cast<T *>(v_pages), *to = static_cast<T *>(out);
-    TraceScope trace("paged_decode", st);
-    const unsigned grid = (unsigned)(B * Hkv);
+    const int64_t most = max_pages * page + 1;
     switch (d) {
-    case 32: k_paged_decode<T, 32><<<grid, 256, 0, st>>>(tq, tk, tv, kp, vp, weights, to, a, dc); break;
-    case 64: k_paged_decode<T, 64><<<grid, 256, 0, st>>>(tq, tk, tv, kp, vp, weights, to, a, dc); break;
-    default: k_paged_decode<T, 128><<<grid, 256, 0, st>>>(tq, tk, tv, kp, vp, weights, to, a, dc); break;
+    case 32: return pick_decode<T, 32>(tq, tk, tv, kp, vp, weights, to, a, dc, most, st);
+    case 64: return pick_decode<T, 64>(tq, tk, tv, kp, vp, weights, to, a, dc, most, st);
+    default: return pick_decode<T, 128>(tq, tk, tv, kp, vp, weights, to, a, dc, most, st);
     }
-    return launched();
 }
 
 // The evicted rows of every (batch, kv head), when they go into a memory.

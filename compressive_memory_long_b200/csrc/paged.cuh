@@ -66,137 +66,5 @@ k_paged_append(const T *__restrict__ k, const T *__restrict__ v, T *k_pages, T *
     if (weights && c == 0) weights[row] = 0.f;
 }
 
-struct DecodeArgs {
-    const float *beta, *M, *z;   // all null: plain attention
-    const double *freq;          // null: no rotation
-    const int64_t *positions;    // [B], or null: lens
-    int H, rot, interleaved;
-    float rot_scale;
-};
-
-// Channel c of one rotated head row.
-template <typename T>
-__device__ __forceinline__ float rotated(const T *x, int c, double pos, const DecodeArgs &a)
-{
-    if (!a.freq || c >= a.rot) return ld_f(x + c);
-    const int half = a.rot / 2, i = a.interleaved ? c / 2 : c % half;
-    const bool second = a.interleaved ? (c & 1) : c >= half;
-    const float2 cs = rotary_turn(pos, a.freq[i], a.rot_scale);
-    const float x1 = ld_f(x + (a.interleaved ? 2 * i : i));
-    const float x2 = ld_f(x + (a.interleaved ? 2 * i + 1 : i + half));
-    return second ? x2 * cs.x + x1 * cs.y : x1 * cs.x - x2 * cs.y;
-}
-
-// One CTA per (batch, kv head): the new row is written, then the group's heads one after the
-// other: eight warps split the rows, each with its own running maximum, sum and values.
-template <typename T, int D>
-__global__ void __launch_bounds__(256)
-k_paged_decode(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v, T *k_pages,
-               T *v_pages, float *weights, T *__restrict__ out, PageArgs a, DecodeArgs dc)
-{
-    constexpr int NW = 8, PL = D / 32;
-    __shared__ float sq[D], sk[D];
-    __shared__ float s_m[NW], s_l[NW], s_o[NW][D], s_den;
-    const int64_t b = blockIdx.x / a.Hkv;
-    const int kvh = (int)(blockIdx.x % a.Hkv), G = dc.H / a.Hkv;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int len = cached_rows(a, b);
-    const int *table = a.table + b * a.max_pages;
-    const int64_t h0 = b * dc.H + (int64_t)kvh * G;
-    if (len < 0) {
-        for (int i = tid; i < G * D; i += 256) st_f(out + h0 * D + i, 0.f);
-        return;
-    }
-    const double pos = dc.positions ? (double)dc.positions[b] : (double)len;
-    const int64_t n = (int64_t)len + (k ? 1 : 0);
-    const T *vt = nullptr;
-    if (k) {
-        const T *kt = k + ((int64_t)b * a.Hkv + kvh) * D;
-        vt = v + ((int64_t)b * a.Hkv + kvh) * D;
-        const int64_t row = pool_row(a, table, len, kvh);
-        for (int c = tid; c < D; c += 256) {
-            T x;
-            st_f(&x, rotated(kt, c, pos, dc));
-            sk[c] = ld_f(&x);
-            if (row >= 0) {
-                k_pages[row * D + c] = x;
-                v_pages[row * D + c] = vt[c];
-            }
-        }
-        if (weights && row >= 0 && tid == 0) weights[row] = 0.f;
-    }
-    const float sl2 = rsqrtf((float)D) * 1.4426950408889634f;
-    for (int g = 0; g < G; ++g) {
-        __syncthreads();
-        for (int c = tid; c < D; c += 256) sq[c] = rotated(q + (h0 + g) * D, c, pos, dc);
-        __syncthreads();
-        float o[PL], m = -INFINITY, l = 0.f;
-#pragma unroll
-        for (int e = 0; e < PL; ++e) o[e] = 0.f;
-        auto score = [&](int64_t j, int64_t &row) {
-            row = j == len ? -1 : pool_row(a, table, j, kvh);
-            if (row < 0 && j != len) return -INFINITY;
-            float part = 0.f;
-#pragma unroll
-            for (int e = 0; e < PL; ++e)
-                part = fmaf(sq[lane + 32 * e], j == len ? sk[lane + 32 * e] : ld_f(k_pages + row * D + lane + 32 * e), part);
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
-            return part * sl2;
-        };
-        for (int64_t j = warp; j < n; j += NW) {
-            int64_t row;
-            const float x = score(j, row);
-            if (x == -INFINITY) continue;
-            const float mn = fmaxf(m, x), r = exp2f(m - mn), p = exp2f(x - mn);
-            l = l * r + p;
-            const T *vr = j == len ? vt : v_pages + row * D;
-#pragma unroll
-            for (int e = 0; e < PL; ++e) o[e] = fmaf(p, ld_f(vr + lane + 32 * e), o[e] * r);
-            m = mn;
-        }
-        if (lane == 0) {
-            s_m[warp] = m;
-            s_l[warp] = l;
-        }
-#pragma unroll
-        for (int e = 0; e < PL; ++e) s_o[warp][lane + 32 * e] = o[e];
-        if (dc.M && warp == 0) {
-            float part = 0.f;
-            for (int f = lane; f < D; f += 32)
-                part = fmaf(feature_map(sq[f]), dc.z[((int64_t)b * a.Hkv + kvh) * D + f], part);
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
-            if (lane == 0) s_den = part;
-        }
-        __syncthreads();
-        float mx = -INFINITY, ls = 0.f;
-        for (int w = 0; w < NW; ++w) mx = fmaxf(mx, s_m[w]);
-        for (int w = 0; w < NW; ++w)
-            if (s_m[w] != -INFINITY) ls = fmaf(s_l[w], exp2f(s_m[w] - mx), ls);
-        if (tid < D) {
-            float os = 0.f;
-            for (int w = 0; w < NW; ++w)
-                if (s_m[w] != -INFINITY) os = fmaf(s_o[w][tid], exp2f(s_m[w] - mx), os);
-            float y = ls > 0.f ? os / ls : 0.f;
-            if (dc.M) {
-                const float *Mc = dc.M + ((int64_t)b * a.Hkv + kvh) * D * D;
-                float num = 0.f;
-                for (int f = 0; f < D; ++f) num = fmaf(feature_map(sq[f]), Mc[f * D + tid], num);
-                const float gt = 1.f / (1.f + expf(-dc.beta[kvh * G + g]));
-                y = gt * (s_den == 0.f ? 0.f : num / s_den) + (1.f - gt) * y;
-            }
-            st_f(out + (h0 + g) * D + tid, y);
-        }
-        if (weights)
-            for (int64_t j = warp; j < n; j += NW) {
-                int64_t row;
-                const float x = score(j, row);
-                if (j == len) row = pool_row(a, table, len, kvh);
-                if (lane == 0 && row >= 0) weights[row] += exp2f(x - mx) / ls;
-            }
-    }
-}
-
 }  // namespace paged
 }  // namespace infini

@@ -1,0 +1,642 @@
+// One new token's attention over a paged cache: split over the rows, then joined.
+//
+// For every query head of a (sequence, key/value head) with rows 0 .. n-1,
+//   s_j = q . k_j / sqrt(d),   m = max_j s_j,   l = sum_j e^(s_j - m),   o = sum_j e^(s_j - m) v_j / l.
+// A piece of the rows gives (m_i, l_i, o_i) of its own; pieces join by
+//   m = max m_i,   l = sum l_i e^(m_i - m),   o = (sum o_i e^(m_i - m)) / l.
+//
+// The work is read bandwidth: 2 d elements per row against 4 d operations per query head.  So
+// the split kernel is one resident wave of CTAs (two per SM) that share all rows of the batch
+// evenly (share.cuh); a unit there is a (sequence, key/value head, tile of up to eight query
+// heads).
+#pragma once
+
+#include "paged.cuh"
+#include "share.cuh"
+
+namespace infini {
+namespace paged {
+
+struct DecodeArgs {
+    const float *beta, *M, *z;   // all null: plain attention
+    const double *freq;          // null: no rotation
+    const int64_t *positions;    // [B], or null: lens
+    int H, rot, interleaved;
+    float rot_scale;
+    int G, HT, hg;               // query heads per kv head; tiles of them; heads per full tile
+    int64_t B;
+    float *part_o, *part_ml;     // [slots, hg, D], [slots, hg, 2]
+    float *scores;               // [P, Hkv, page, G], base-2 scaled (null without weights)
+};
+
+constexpr int kSplitCtas = 296;      // two on each of 148 SMs
+constexpr int kSplitWarps = 4;
+constexpr int kStages = 3;
+
+// A warp stages 4 KB of keys and 4 KB of values at a time.
+template <typename T, int D>
+struct DecodeTile {
+    static constexpr int CPR = D * (int)sizeof(T) / 16;   // 16-byte chunks of a row
+    static constexpr int R = 256 / CPR;                   // rows a warp stages
+    static constexpr int TR = kSplitWarps * R;            // rows of a tile
+    static constexpr int RL = (R + 31) / 32;
+    // Chunk c of row r sits at c ^ swz(r), so that eight rows' chunk c lie in eight different
+    // groups of four banks.
+    static __device__ __forceinline__ int swz(int r) { return CPR >= 8 ? (r & 7) : ((r >> 1) & 3); }
+};
+
+__device__ __forceinline__ int64_t unit_rows(const PageArgs &a, int64_t b, int extra)
+{
+    const int len = cached_rows(a, b);
+    return len < 0 ? 0 : (int64_t)len + extra;
+}
+
+// ---- rotation and small pieces ----------------------------------------------------------------
+
+// Channel c of one rotated head row.
+template <typename T>
+__device__ __forceinline__ float rotated(const T *x, int c, double pos, const DecodeArgs &a)
+{
+    if (!a.freq || c >= a.rot) return ld_f(x + c);
+    const int half = a.rot / 2, i = a.interleaved ? c / 2 : c % half;
+    const bool second = a.interleaved ? (c & 1) : c >= half;
+    const float2 cs = rotary_turn(pos, a.freq[i], a.rot_scale);
+    const float x1 = ld_f(x + (a.interleaved ? 2 * i : i));
+    const float x2 = ld_f(x + (a.interleaved ? 2 * i + 1 : i + half));
+    return second ? x2 * cs.x + x1 * cs.y : x1 * cs.x - x2 * cs.y;
+}
+
+// Rows g0 .. g0 + heads - 1 of q, rotated, into sq [heads][D]; one thread turns a pair of
+// channels of all heads.  Rows up to `fill` are set to 0.
+template <typename T, int D, int NT>
+__device__ __forceinline__ void load_q(const T *__restrict__ q, int heads, int fill, double pos,
+                                       const DecodeArgs &a, float *sq)
+{
+    const int half = a.freq ? a.rot / 2 : 0;
+    for (int i = threadIdx.x; i < D / 2; i += NT) {
+        int c1 = 2 * i, c2 = 2 * i + 1;
+        float2 cs = make_float2(1.f, 0.f);
+        if (i < half) {
+            if (!a.interleaved) {
+                c1 = i;
+                c2 = i + half;
+            }
+            cs = rotary_turn(pos, a.freq[i], a.rot_scale);
+        }
+        for (int g = 0; g < heads; ++g) {
+            const float x1 = ld_f(q + g * D + c1), x2 = ld_f(q + g * D + c2);
+            sq[g * D + c1] = x1 * cs.x - x2 * cs.y;
+            sq[g * D + c2] = x2 * cs.x + x1 * cs.y;
+        }
+    }
+    for (int i = heads * D + threadIdx.x; i < fill * D; i += NT) sq[i] = 0.f;
+}
+
+__device__ __forceinline__ uint32_t s_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// 16 bytes global -> shared, zeros where !ok (the source is not read then).
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok)
+{
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
+                 : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4_t(uint32_t a, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two values as bf16 pairs hi and lo with hi + lo = x to 2^-17 of it.
+__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    const __nv_bfloat162 l = __floats2bfloat162_rn(x - __bfloat162float(h.x), y - __bfloat162float(h.y));
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+
+// ---- the split kernel ---------------------------------------------------------------------------
+//
+// Four warps; each stages its own rows with cp.async three deep (up to 24 KB a warp, 192 KB an
+// SM, in flight) and needs no barrier inside a piece.  The stages run on across pieces, so a
+// unit's end drains nothing.
+//
+// bf16: products on mma.sync m16n8k16 with the query heads as the 16 rows: rows 0-7 hold eight
+// heads' high bf16 part and rows 8-15 their low part (q after rotation, and the weights e^(s-m),
+// are 32-bit values).  Both parts of a head land in one thread, which adds them: the split costs
+// no instruction, and eight heads are the tile.  The tensor rate is no bound here (104 TFLOP/s
+// at full read bandwidth).
+//
+// fp32: on the CUDA cores, exactly; GT query heads at a time.  A lane forms a quarter of one
+// row's dot products, and a float4 column of the values' sum.
+template <typename T, int D, int GT>
+__global__ void __launch_bounds__(32 * kSplitWarps, 2)
+k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v, T *k_pages,
+               T *v_pages, PageArgs a, DecodeArgs dc)
+{
+    using Tile = DecodeTile<T, D>;
+    constexpr bool kMma = sizeof(T) == 2;
+    constexpr int CPR = Tile::CPR, R = Tile::R, TR = Tile::TR, RL = Tile::RL, NT = 32 * kSplitWarps;
+    constexpr int NO = D / 8;                              // mma: accumulator tiles of 8 channels
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ float s_m[kSplitWarps][8], s_l[kSplitWarps][8];
+    __shared__ ShareScratch s_share;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    unsigned char *stages = smem;                                                // [warp][stage][8 KB]
+    float *sq = reinterpret_cast<float *>(smem + kSplitWarps * kStages * 8192);   // [GT][D]
+    float *s_o = sq + GT * D;                                                    // [2][GT][D]
+    int64_t *s_base = reinterpret_cast<int64_t *>(s_o + 2 * GT * D);             // [warp][stage][R]
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int extra = k ? 1 : 0, KH = a.Hkv * dc.HT;
+    const int64_t cta = blockIdx.x;
+
+    int64_t t0, t1;
+    Walk rd;
+    auto rows_of = [&](int64_t b) { return unit_rows(a, b, extra); };
+    share_begin<kSplitCtas, NT>(rows_of, dc.B, KH, TR, s_share, t0, t1, rd);
+    if (t0 >= t1) return;                // the whole CTA
+    Walk ld = rd;
+    int64_t t_ld = t0;
+
+    unsigned char *my = stages + warp * kStages * 8192;
+    int64_t *my_base = s_base + warp * kStages * R;
+    int pg[RL];
+    // page numbers of the next tile to load, one tile ahead of their use
+    auto fetch_pages = [&] {
+#pragma unroll
+        for (int e = 0; e < RL; ++e) {
+            pg[e] = -1;
+            const int64_t r = ld.tile * TR + warp * R + lane + 32 * e;
+            if (t_ld < t1 && lane + 32 * e < R && r < ld.n) {
+                const int64_t i = r >> a.shift;
+                pg[e] = i < a.max_pages ? a.table[ld.b * a.max_pages + i] : -1;
+            }
+        }
+    };
+    auto issue = [&](int stage) {
+        if (t_ld < t1) {
+            const int kvh = ld.kh / dc.HT;
+            const int64_t r0 = ld.tile * TR + warp * R, len = ld.n - extra;
+            int64_t base[RL];
+#pragma unroll
+            for (int e = 0; e < RL; ++e) {
+                const int64_t r = r0 + lane + 32 * e;
+                base[e] = -1;
+                if (lane + 32 * e < R && r < ld.n) {
+                    if (pg[e] >= 0 && pg[e] < a.P)
+                        base[e] = ((((int64_t)pg[e] * a.Hkv + kvh) << a.shift) |
+                                   (r & (((int64_t)1 << a.shift) - 1)));
+                    else
+                        g_page_status = 1;
+                }
+                if (lane + 32 * e < R) my_base[stage * R + lane + 32 * e] = base[e];
+                if (r >= len) base[e] = -1;                // the new row comes from k and v
+            }
+            const uint32_t dk = s_u32(my + stage * 8192);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int ci = i * 32 + lane, r = ci / CPR, c = ci % CPR;
+                const int64_t at = __shfl_sync(0xffffffffu, base[RL == 1 ? 0 : (i * 32 / CPR) / 32], r & 31);
+                const int64_t off = (at < 0 ? 0 : at * D) + c * (16 / (int)sizeof(T));
+                const uint32_t dst = dk + (r * CPR + (c ^ Tile::swz(r))) * 16;
+                cp16(dst, k_pages + off, at >= 0);
+                cp16(dst + 4096, v_pages + off, at >= 0);
+            }
+            walk_next(ld, rows_of, KH, dc.B, TR);
+            ++t_ld;
+            fetch_pages();
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    fetch_pages();
+    for (int s = 0; s < kStages - 1; ++s) issue(s);
+
+    const float sl2 = rsqrtf((float)D) * 1.4426950408889634f;
+    float m[kMma ? 1 : GT], l[kMma ? 1 : GT];
+    float o[kMma ? NO : GT][4];
+    uint32_t qa[kMma ? D / 16 : 1][4];
+
+    for (int64_t t = t0; t < t1; ++t) {
+        const int stage = (int)((t - t0) % kStages);
+        issue((int)((t - t0 + kStages - 1) % kStages));
+        const int kvh = rd.kh / dc.HT, ht = rd.kh % dc.HT;
+        const int heads = min(dc.G - ht * dc.hg, dc.hg);
+        const int64_t h0 = rd.b * dc.H + (int64_t)kvh * dc.G + ht * dc.hg;
+        const int64_t len = rd.n - extra;
+        const double pos = !dc.freq ? 0.0 : dc.positions ? (double)dc.positions[rd.b] : (double)len;
+        if (t == t0 || rd.tile == 0) {                     // a piece begins
+            load_q<T, D, NT>(q + h0 * D, heads, GT, pos, dc, sq);
+            __syncthreads();
+            if constexpr (kMma) {
+                const float *row = sq + (lane >> 2) * D + (lane & 3) * 2;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    split2(row[i * 16], row[i * 16 + 1], qa[i][0], qa[i][1]);
+                    split2(row[i * 16 + 8], row[i * 16 + 9], qa[i][2], qa[i][3]);
+                }
+            }
+#pragma unroll
+            for (int g = 0; g < (kMma ? 1 : GT); ++g) {
+                m[g] = -INFINITY;
+                l[g] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < (kMma ? NO : GT); ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        __syncwarp();
+        unsigned char *sk = my + stage * 8192, *sv = sk + 4096;
+        const int64_t *bs = my_base + stage * R;
+        const int64_t r0 = rd.tile * TR + warp * R;
+        const int mine = (int)min((int64_t)R, rd.n - r0);   // rows of this warp (none: <= 0)
+        if (extra && r0 <= len && len < r0 + R) {
+            // the new row: rotated, rounded to the cache's type, into the stage and its page
+            const int j = (int)(len - r0);
+            const int64_t src = (rd.b * a.Hkv + kvh) * D, at = bs[j];
+            for (int c = lane; c < D; c += 32) {
+                T x;
+                st_f(&x, rotated(k + src, c, pos, dc));
+                const T y = v[src + c];
+                const int e = 16 / (int)sizeof(T), p = (j * CPR + ((c / e) ^ Tile::swz(j))) * e + c % e;
+                reinterpret_cast<T *>(sk)[p] = x;
+                reinterpret_cast<T *>(sv)[p] = y;
+                if (at >= 0 && ht == 0) {
+                    k_pages[at * D + c] = x;
+                    v_pages[at * D + c] = y;
+                }
+            }
+            __syncwarp();
+        }
+        auto valid = [&](int j) { return j < mine && (bs[j] >= 0 || r0 + j == len); };
+        if constexpr (kMma) {
+            const uint32_t ka = s_u32(sk), va = s_u32(sv);
+            for (int rb = 0; rb < R && rb < mine; rb += 16) {
+                float s[2][4] = {};
+                // keys: matrices (rows 0-7, k 0-7), (rows 0-7, k 8-15), (rows 8-15, ...) x 2
+                const int kr = rb + ((lane >> 4) << 3) + (lane & 7), kc = (lane >> 3) & 1;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    uint32_t b[4];
+                    ldsm4(ka + (kr * CPR + ((2 * i + kc) ^ Tile::swz(kr))) * 16, b);
+                    mma16816(s[0], qa[i], b[0], b[1]);
+                    mma16816(s[1], qa[i], b[2], b[3]);
+                }
+                float x[2][2], mx = m[0];
+#pragma unroll
+                for (int n8 = 0; n8 < 2; ++n8)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int j = rb + n8 * 8 + (lane & 3) * 2 + e;
+                        const bool ok = valid(j);
+                        x[n8][e] = ok ? (s[n8][e] + s[n8][e + 2]) * sl2 : -INFINITY;
+                        mx = fmaxf(mx, x[n8][e]);
+                        if (dc.scores && (lane >> 2) < heads && ok && bs[j] >= 0)
+                            dc.scores[bs[j] * dc.G + ht * dc.hg + (lane >> 2)] = x[n8][e];
+                    }
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const float at = mx == -INFINITY ? 0.f : mx, corr = exp2f(m[0] - at);
+                uint32_t pa[4];
+                float p[2][2];
+#pragma unroll
+                for (int n8 = 0; n8 < 2; ++n8) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) p[n8][e] = exp2f(x[n8][e] - at);
+                    split2(p[n8][0], p[n8][1], pa[2 * n8], pa[2 * n8 + 1]);
+                }
+                l[0] = l[0] * corr + ((p[0][0] + p[0][1]) + (p[1][0] + p[1][1]));
+                m[0] = mx;
+                if (__any_sync(0xffffffffu, corr != 1.f)) {
+#pragma unroll
+                    for (int i = 0; i < NO; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[i][e] *= corr;
+                }
+                // values: matrices (rows 0-7, c 0-7), (rows 8-15, c 0-7), (rows 0-7, c 8-15), ...
+                const int vr = rb + (lane & 15), vc = lane >> 4;
+#pragma unroll
+                for (int i = 0; i < NO / 2; ++i) {
+                    uint32_t b[4];
+                    ldsm4_t(va + (vr * CPR + ((2 * i + vc) ^ Tile::swz(vr))) * 16, b);
+                    mma16816(o[2 * i], pa, b[0], b[1]);
+                    mma16816(o[2 * i + 1], pa, b[2], b[3]);
+                }
+            }
+        } else {
+            const float4 *kf = reinterpret_cast<const float4 *>(sk), *vf = reinterpret_cast<const float4 *>(sv);
+            const float4 *qf = reinterpret_cast<const float4 *>(sq);
+            const int r = lane & 7, part = lane >> 3;
+            for (int rb = 0; rb < R && rb < mine; rb += 8) {
+                float s[GT];
+#pragma unroll
+                for (int g = 0; g < GT; ++g) s[g] = 0.f;
+#pragma unroll
+                for (int i = 0; i < CPR / 4; ++i) {
+                    const int c = 4 * i + part;
+                    const float4 y = kf[(rb + r) * CPR + (c ^ r)];
+#pragma unroll
+                    for (int g = 0; g < GT; ++g) {
+                        const float4 w = qf[g * CPR + c];
+                        s[g] = fmaf(y.x, w.x, fmaf(y.y, w.y, fmaf(y.z, w.z, fmaf(y.w, w.w, s[g]))));
+                    }
+                }
+                const bool ok = valid(rb + r);
+                float p[GT];
+#pragma unroll
+                for (int g = 0; g < GT; ++g) {
+                    s[g] += __shfl_xor_sync(0xffffffffu, s[g], 8);
+                    s[g] += __shfl_xor_sync(0xffffffffu, s[g], 16);
+                    const float x = ok ? s[g] * sl2 : -INFINITY;
+                    if (dc.scores && part == 0 && g < heads && ok && bs[rb + r] >= 0)
+                        dc.scores[bs[rb + r] * dc.G + ht * dc.hg + g] = x;
+                    float mx = x;
+#pragma unroll
+                    for (int off = 1; off < 8; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                    mx = fmaxf(mx, m[g]);
+                    const float at = mx == -INFINITY ? 0.f : mx, corr = exp2f(m[g] - at);
+                    p[g] = exp2f(x - at);
+                    l[g] = l[g] * corr + p[g];
+                    m[g] = mx;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[g][e] *= corr;
+                }
+                constexpr int RW = 32 / CPR;               // rows of the values read at once
+                const int c = lane % CPR, sub = lane / CPR;
+#pragma unroll
+                for (int j = 0; j < 8 / RW; ++j) {
+                    const int row = j * RW + sub;
+                    const float4 y = vf[(rb + row) * CPR + (c ^ row)];
+#pragma unroll
+                    for (int g = 0; g < GT; ++g) {
+                        const float w = __shfl_sync(0xffffffffu, p[g], row);
+                        o[g][0] = fmaf(w, y.x, o[g][0]);
+                        o[g][1] = fmaf(w, y.y, o[g][1]);
+                        o[g][2] = fmaf(w, y.z, o[g][2]);
+                        o[g][3] = fmaf(w, y.w, o[g][3]);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        if (t == t1 - 1 || rd.tile == rd.nt - 1) {         // a piece ends: join the warps
+            if constexpr (kMma) {
+                l[0] += __shfl_xor_sync(0xffffffffu, l[0], 1);
+                l[0] += __shfl_xor_sync(0xffffffffu, l[0], 2);
+                if ((lane & 3) == 0) {
+                    s_m[warp][lane >> 2] = m[0];
+                    s_l[warp][lane >> 2] = l[0];
+                }
+            } else {
+#pragma unroll
+                for (int g = 0; g < GT; ++g) {
+#pragma unroll
+                    for (int off = 1; off < 8; off <<= 1) l[g] += __shfl_xor_sync(0xffffffffu, l[g], off);
+#pragma unroll
+                    for (int off = CPR; off < 32; off <<= 1)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[g][e] += __shfl_xor_sync(0xffffffffu, o[g][e], off);
+                    if (lane == 0) {
+                        s_m[warp][g] = m[g];
+                        s_l[warp][g] = l[g];
+                    }
+                }
+            }
+            __syncthreads();
+            auto top = [&](int g) {
+                float mx = s_m[0][g];
+#pragma unroll
+                for (int w = 1; w < kSplitWarps; ++w) mx = fmaxf(mx, s_m[w][g]);
+                return mx;
+            };
+            auto share = [&](int w, int g, float mx) {
+                return mx == -INFINITY ? 0.f : exp2f(s_m[w][g] - mx);
+            };
+#pragma unroll
+            for (int turn = 0; turn < 2; ++turn) {         // warps 0, 1, then 2, 3 on top of them
+                if (warp / 2 == turn) {
+                    float *dst = s_o + (warp & 1) * GT * D;
+                    if constexpr (kMma) {
+                        const int g = lane >> 2;
+                        const float f = share(warp, g, top(g));
+#pragma unroll
+                        for (int i = 0; i < NO; ++i)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float *y = dst + g * D + i * 8 + (lane & 3) * 2 + e;
+                                const float x = (o[i][e] + o[i][e + 2]) * f;
+                                *y = turn ? *y + x : x;
+                            }
+                    } else {
+#pragma unroll
+                        for (int g = 0; g < GT; ++g) {
+                            const float f = share(warp, g, top(g));
+                            if (lane < CPR)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    float *y = dst + g * D + lane * 4 + e;
+                                    *y = turn ? *y + o[g][e] * f : o[g][e] * f;
+                                }
+                        }
+                    }
+                }
+                __syncthreads();
+            }
+            const int64_t slot = cta + rd.b * KH + rd.kh;
+            float *po = dc.part_o + slot * dc.hg * D;
+            for (int i = tid; i < heads * D; i += NT) po[i] = s_o[i] + s_o[GT * D + i];
+            if (tid < heads) {
+                const float mx = top(tid);
+                float ls = 0.f;
+#pragma unroll
+                for (int w = 0; w < kSplitWarps; ++w) ls = fmaf(s_l[w][tid], share(w, tid, mx), ls);
+                dc.part_ml[(slot * dc.hg + tid) * 2] = mx;
+                dc.part_ml[(slot * dc.hg + tid) * 2 + 1] = ls;
+            }
+        }
+        walk_next(rd, rows_of, KH, dc.B, TR);
+    }
+}
+
+// ---- the join -----------------------------------------------------------------------------------
+//
+// One CTA per (sequence, key/value head) and chunk of rows.  Chunk 0 reads the memory (before it
+// waits for the split kernel: it depends on the inputs alone), joins the pieces, gates and writes
+// the output; with weights, every chunk adds its rows' normalised weights from the kept scores.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 1024;      // rows of a chunk
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads)
+k_paged_join(const T *__restrict__ q, float *weights, T *__restrict__ out, PageArgs a, DecodeArgs dc, int extra)
+{
+    constexpr int TR = DecodeTile<T, D>::TR, NT = kJoinThreads, NW = NT / 32, C4 = D / 4;
+    __shared__ __align__(16) float sq[8 * D], s_num[8 * D];
+    __shared__ float s_den[8], s_mx[8], s_il[8];
+    __shared__ ShareScratch s_share;
+    const int64_t b = blockIdx.x / a.Hkv;
+    const int kvh = (int)(blockIdx.x % a.Hkv), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int KH = a.Hkv * dc.HT;
+    const int len = cached_rows(a, b);
+    const int64_t n = len < 0 ? 0 : (int64_t)len + extra;
+    const int64_t h0 = b * dc.H + (int64_t)kvh * dc.G;
+    // every path waits for the split kernel, so that no grid of this stream ends before it
+    auto wait_split = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
+    if (blockIdx.y > 0 && (int64_t)blockIdx.y * kJoinRows >= n) {
+        wait_split();
+        return;
+    }
+    if (len < 0) {
+        for (int i = tid; i < dc.G * D; i += NT) st_f(out + h0 * D + i, 0.f);
+        wait_split();
+        return;
+    }
+    const int64_t unit_b = b * a.Hkv + kvh;
+    int64_t before;
+    auto rows_of = [&](int64_t i) { return unit_rows(a, i, extra); };
+    const int64_t total = KH * share_count<NT>(rows_of, dc.B, TR, b, s_share, before);
+    const int64_t nt = (n + TR - 1) / TR;
+    const double pos = !dc.freq ? 0.0 : dc.positions ? (double)dc.positions[b] : (double)len;
+    for (int ht = 0; ht < dc.HT; ++ht) {
+        const int heads = min(dc.G - ht * dc.hg, dc.hg);
+        if (dc.M && blockIdx.y == 0) {
+            // num_g = sigma(q_g) M, den_g = sigma(q_g) . z: a warp takes every NW-th row of M,
+            // a lane C4-th of it; the warps' sums meet one after the other
+            __syncthreads();
+            load_q<T, D, NT>(q + (h0 + ht * dc.hg) * D, heads, 8, pos, dc, sq);
+            __syncthreads();
+            for (int i = tid; i < 8 * D; i += NT) sq[i] = i < heads * D ? feature_map(sq[i]) : 0.f;
+            __syncthreads();
+            constexpr int RW = 32 / C4;                    // rows of M a warp reads at once
+            float4 acc[8];
+#pragma unroll
+            for (int g = 0; g < 8; ++g) acc[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 *Mf = reinterpret_cast<const float4 *>(dc.M + unit_b * D * D);
+            const int c = lane % C4, sub = lane / C4;
+#pragma unroll 4
+            for (int f = warp * RW + sub; f < D; f += NW * RW) {
+                const float4 y = __ldcs(Mf + f * C4 + c);
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    const float w = sq[g * D + f];
+                    acc[g].x = fmaf(w, y.x, acc[g].x);
+                    acc[g].y = fmaf(w, y.y, acc[g].y);
+                    acc[g].z = fmaf(w, y.z, acc[g].z);
+                    acc[g].w = fmaf(w, y.w, acc[g].w);
+                }
+            }
+            if (warp < heads) {
+                float part = 0.f;
+                for (int f = lane; f < D; f += 32) part = fmaf(sq[warp * D + f], dc.z[unit_b * D + f], part);
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
+                if (lane == 0) s_den[warp] = part;
+            }
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+#pragma unroll
+                for (int off = C4; off < 32; off <<= 1) {
+                    acc[g].x += __shfl_xor_sync(0xffffffffu, acc[g].x, off);
+                    acc[g].y += __shfl_xor_sync(0xffffffffu, acc[g].y, off);
+                    acc[g].z += __shfl_xor_sync(0xffffffffu, acc[g].z, off);
+                    acc[g].w += __shfl_xor_sync(0xffffffffu, acc[g].w, off);
+                }
+            for (int w = 0; w < NW; ++w) {
+                if (warp == w && lane < C4)
+#pragma unroll
+                    for (int g = 0; g < 8; ++g) {
+                        float4 *y = reinterpret_cast<float4 *>(s_num + g * D) + lane;
+                        float4 x = acc[g];
+                        if (w > 0) {
+                            const float4 z = *y;
+                            x = make_float4(x.x + z.x, x.y + z.y, x.z + z.z, x.w + z.w);
+                        }
+                        *y = x;
+                    }
+                __syncthreads();
+            }
+        }
+        if (ht == 0) wait_split();
+        // the unit's pieces: CTAs c0 .. c1 of the split kernel
+        const int64_t unit = b * KH + kvh * dc.HT + ht;
+        int64_t c0 = 0, c1 = -1;
+        if (n > 0) {
+            const int64_t s = before * KH + (kvh * dc.HT + ht) * nt;
+            c0 = share_owner<kSplitCtas>(s, total);
+            c1 = share_owner<kSplitCtas>(s + nt - 1, total);
+        }
+        __syncthreads();
+        if (warp < heads) {
+            // (a maximum of -inf: no row, or NaN alone, which stays in the sums)
+            float mx = -INFINITY, ls = 0.f;
+            for (int64_t c = c0 + lane; c <= c1; c += 32)
+                mx = fmaxf(mx, dc.part_ml[((c + unit) * dc.hg + warp) * 2]);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            for (int64_t c = c0 + lane; c <= c1; c += 32) {
+                const float *ml = dc.part_ml + ((c + unit) * dc.hg + warp) * 2;
+                ls = fmaf(ml[1], mx == -INFINITY ? 0.f : exp2f(ml[0] - mx), ls);
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, off);
+            if (lane == 0) {
+                s_mx[warp] = mx;
+                s_il[warp] = ls == 0.f ? 0.f : 1.f / ls;
+            }
+        }
+        __syncthreads();
+        if (blockIdx.y == 0) {
+            for (int i = tid; i < heads * D; i += NT) {
+                const int g = i / D;
+                const float mx = s_mx[g];
+                float y = 0.f;
+#pragma unroll 4
+                for (int64_t c = c0; c <= c1; ++c)
+                    y = fmaf(dc.part_o[(c + unit) * dc.hg * D + i],
+                             mx == -INFINITY ? 0.f : exp2f(dc.part_ml[((c + unit) * dc.hg + g) * 2] - mx), y);
+                y *= s_il[g];
+                if (dc.M) {
+                    const float gt = 1.f / (1.f + expf(-dc.beta[kvh * dc.G + ht * dc.hg + g]));
+                    y = gt * (s_den[g] == 0.f ? 0.f : s_num[i] / s_den[g]) + (1.f - gt) * y;
+                }
+                st_f(out + (h0 + ht * dc.hg) * D + i, y);
+            }
+        }
+        if (weights) {
+            const int *table = a.table + b * a.max_pages;
+            for (int64_t j0 = (int64_t)blockIdx.y * kJoinRows; j0 < n; j0 += (int64_t)gridDim.y * kJoinRows)
+#pragma unroll
+                for (int e = 0; e < kJoinRows / NT; ++e) {
+                    const int64_t j = j0 + e * NT + tid;
+                    const int64_t row = j < n ? pool_row(a, table, j, kvh) : -1;
+                    if (row < 0) continue;
+                    float sum = 0.f;
+                    const float *x = dc.scores + row * dc.G + ht * dc.hg;
+                    for (int g = 0; g < heads; ++g)
+                        sum = fmaf(s_mx[g] == -INFINITY ? 0.f : exp2f(x[g] - s_mx[g]), s_il[g], sum);
+                    weights[row] = j == len && ht == 0 ? sum : weights[row] + sum;
+                }
+        }
+    }
+}
+
+}  // namespace paged
+}  // namespace infini
