@@ -5,9 +5,15 @@
 // The kept rows, in their old order, are copied to the first rows of the sequence's
 // destination pages.  With a memory the other rows are folded into it as one update of the
 // linear rule, M += sum sigma(k) v^T and z += sum sigma(k).
+//
+// Three steps, each a kernel that may start while the one before drains: select (cluster of
+// CTAs per head, the weights read once), fold (tensor cores, the evicted rows shared out over
+// all SMs, then a reduction of the pieces), move.
 #pragma once
 
 #include "paged.cuh"
+#include "share.cuh"
+#include "tc_common.cuh"
 
 namespace infini {
 namespace paged {
@@ -16,8 +22,10 @@ struct EvictArgs {
     const int *dst_table;        // [B, dst_pages]
     int dst_pages, budget, recent;
     int *lens_out, *kept;        // [B], [B, Hkv, budget]
-    int *gone;                   // [B, Hkv, rows - budget] evicted rows (with a memory)
+    int *gone;                   // [B, Hkv, gone_stride] evicted rows (with a memory)
     int64_t gone_stride;
+    int64_t B;
+    float *part_M, *part_z;      // [slots, D * D], [slots, kFoldLoaders, D]
 };
 
 // Order-preserving image of a float: larger weight, larger key.  NaN sorts above everything,
@@ -29,153 +37,587 @@ __device__ __forceinline__ uint32_t weight_key(float w)
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// One CTA per (batch, kv head).  The weight of rank m is found digit by digit from the top
-// (four passes of 8 bits over the candidates, each a histogram of those that share the digits
-// found so far); one more pass writes the kept rows, counting rows before each by a block
-// prefix sum.
-__global__ void __launch_bounds__(1024)
-k_evict_select(const float *__restrict__ weights, PageArgs a, EvictArgs e)
+// ---- select -----------------------------------------------------------------------------------
+//
+// A cluster of CTAs per (batch, kv head); each holds the keys of its part of the rows in shared
+// memory (rows past kSelectKeys are read again).  The key of rank m is found digit by digit from
+// the top: 11, 11 and 10 bits, each a histogram of the keys that share the digits found so far,
+// summed over the cluster.  Then every warp counts the keys above and equal to it in its own run
+// of rows; prefix sums over warps and CTAs give each row its place.  11 bits for the first digit
+// take the exponent and two bits more: attention weights spread over few exponents, and 8 bits
+// would put most of them in a handful of bins.
+constexpr int kSelectThreads = 1024;
+constexpr int kSelectKeys = 40960;
+constexpr int kBins = 2048;
+
+__device__ __forceinline__ uint32_t cluster_rank()
 {
-    __shared__ int hist[256];
-    __shared__ int s_scan[2][32];
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+__device__ __forceinline__ int peer_ld(const int *p, uint32_t rank)
+{
+    uint32_t at;
+    int v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+
+__global__ void __launch_bounds__(kSelectThreads)
+k_evict_select(const float *__restrict__ weights, PageArgs a, EvictArgs e, int CS, int cap)
+{
+    constexpr int NT = kSelectThreads, NW = NT / 32;
+    extern __shared__ int s_dyn[];
+    int *hist = s_dyn;                                               // [3][kBins]
+    uint32_t *keys = reinterpret_cast<uint32_t *>(s_dyn + 3 * kBins);   // [cap]
+    __shared__ int s_warp[NW], s_gt[NW], s_eq[NW], s_tot[2];
     __shared__ int s_digit, s_rank;
-    const int64_t unit = blockIdx.x, b = unit / a.Hkv;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t unit = blockIdx.x / CS, b = unit / a.Hkv;
     const int kvh = (int)(unit % a.Hkv), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = CS > 1 ? (int)cluster_rank() : 0;
     const int n = cached_rows(a, b);
     const int *table = a.table + b * a.max_pages;
     int *kept = e.kept + unit * e.budget;
-    if (tid == 0 && kvh == 0) e.lens_out[b] = min(n, e.budget);
+    if (tid == 0 && kvh == 0 && rank == 0) e.lens_out[b] = min(n, e.budget);
     if (n <= e.budget) {
-        for (int i = tid; i < e.budget; i += 1024) kept[i] = i < n ? i : -1;
+        for (int64_t i = rank * NT + tid; i < e.budget; i += CS * NT) kept[i] = i < n ? (int)i : -1;
         return;
     }
     const int old = n - min(e.recent, n), m = e.budget - (n - old);   // keep m of rows 0..old-1
-    auto key_of = [&](int r) {
-        const int64_t row = pool_row(a, table, r, kvh);
+    for (int i = rank * NT + tid; i < n - old; i += CS * NT) kept[m + i] = old + i;
+    const int per = (old + CS - 1) / CS, r0 = min(rank * per, old), cnt = min(per, old - r0);
+    auto load_key = [&](int i) {
+        const int64_t row = pool_row(a, table, r0 + i, kvh);
         return row < 0 ? 0u : weight_key(weights[row]);
     };
+    auto key_of = [&](int i) { return i < cap ? keys[i] : load_key(i); };
+    for (int i = tid; i < 3 * kBins; i += NT) hist[i] = 0;
+    {
+        const int held = min(cnt, cap);
+        for (int i0 = tid; i0 < held; i0 += 4 * NT) {
+            uint32_t x[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) x[u] = i0 + u * NT < held ? load_key(i0 + u * NT) : 0;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i0 + u * NT < held) keys[i0 + u * NT] = x[u];
+        }
+    }
+    __syncthreads();
     uint32_t thr = 0;
-    int rank = m;                       // how many keys of the chosen prefix are kept
+    int left = m;                       // how many keys of the digits so far are kept
     if (m > 0) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < 256; i += 1024) hist[i] = 0;
-            __syncthreads();
-            for (int r = tid; r < old; r += 1024) {
-                const uint32_t key = key_of(r);
-                if (shift == 24 || (key >> (shift + 8)) == (thr >> (shift + 8)))
-                    atomicAdd(&hist[(key >> shift) & 255], 1);
+#pragma unroll 1
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+            int *h = hist + pass * kBins;
+            for (int i = tid; i < cnt; i += NT) {
+                const uint32_t key = key_of(i);
+                if (pass == 0 || (key >> (shift + bits)) == (thr >> (shift + bits)))
+                    atomicAdd(&h[(key >> shift) & ((1 << bits) - 1)], 1);
             }
+            if (CS > 1) cluster_sync();
+            else __syncthreads();
+            // bins from the top, two per thread: thread tid has bins 2047 - 2 tid and the next
+            int x0 = 0, x1 = 0;
+            const int top = kBins - 1 - 2 * tid;
+            for (int c = 0; c < CS; ++c) {
+                x0 += CS > 1 ? peer_ld(h + top, c) : h[top];
+                x1 += CS > 1 ? peer_ld(h + top - 1, c) : h[top - 1];
+            }
+            int inc = x0 + x1;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, inc, off);
+                if (lane >= off) inc += y;
+            }
+            if (lane == 31) s_warp[warp] = inc;
             __syncthreads();
-            if (tid == 0) {
-                int left = rank, d = 255;
-                while (d > 0 && hist[d] < left) left -= hist[d--];
-                s_digit = d;
-                s_rank = left;
+            int above = inc - x0 - x1;
+            for (int w = 0; w < warp; ++w) above += s_warp[w];
+            // the digit: the bin where the count from the top reaches `left`
+            if (above < left && left <= above + x0 + x1) {
+                const bool first = left <= above + x0;
+                s_digit = first ? top : top - 1;
+                s_rank = left - above - (first ? 0 : x0);
             }
             __syncthreads();
             thr |= (uint32_t)s_digit << shift;
-            rank = s_rank;
+            left = s_rank;
         }
     }
-    // keys above thr are kept, and the first `rank` of those equal to it
-    int base_keep = 0, base_eq = 0;
+    // a warp's run of rows, 32 at a time
+    const int run = ((cnt + NW - 1) / NW + 31) / 32 * 32, w0 = min(warp * run, cnt), w1 = min(w0 + run, cnt);
+    int gt = 0, eq = 0;
+    for (int i = w0; i < w1; i += 32) {
+        const uint32_t key = i + lane < w1 ? key_of(i + lane) : 0;
+        const bool in = i + lane < w1 && m > 0;
+        gt += __popc(__ballot_sync(0xffffffffu, in && key > thr));
+        eq += __popc(__ballot_sync(0xffffffffu, in && key == thr));
+    }
+    if (lane == 0) {
+        s_gt[warp] = gt;
+        s_eq[warp] = eq;
+    }
+    __syncthreads();
+    if (tid < 2) {
+        int sum = 0;
+        for (int w = 0; w < NW; ++w) sum += tid == 0 ? s_gt[w] : s_eq[w];
+        s_tot[tid] = sum;
+    }
+    if (CS > 1) cluster_sync();
+    else __syncthreads();
+    gt = eq = 0;
+    for (int c = 0; c < rank; ++c) {
+        gt += peer_ld(&s_tot[0], c);
+        eq += peer_ld(&s_tot[1], c);
+    }
+    for (int w = 0; w < warp; ++w) {
+        gt += s_gt[w];
+        eq += s_eq[w];
+    }
     int *gone = e.gone ? e.gone + unit * e.gone_stride : nullptr;
-    for (int r0 = 0; r0 < n; r0 += 1024) {
-        const int r = r0 + tid;
-        const uint32_t key = r < old ? key_of(r) : 0;
-        const bool eq = m > 0 && r < old && key == thr;
-        const unsigned be = __ballot_sync(0xffffffffu, eq);
-        if (lane == 0) s_scan[0][warp] = __popc(be);
-        __syncthreads();
-        int before_eq = base_eq + __popc(be & ((1u << lane) - 1)), all_eq = 0;
-        for (int w = 0; w < 32; ++w) {
-            before_eq += w < warp ? s_scan[0][w] : 0;
-            all_eq += s_scan[0][w];
-        }
-        const bool keep = r < n && (r >= old || (m > 0 && (key > thr || (eq && before_eq < rank))));
-        const unsigned bk = __ballot_sync(0xffffffffu, keep);
-        if (lane == 0) s_scan[1][warp] = __popc(bk);
-        __syncthreads();
-        int before = base_keep + __popc(bk & ((1u << lane) - 1)), all = 0;
-        for (int w = 0; w < 32; ++w) {
-            before += w < warp ? s_scan[1][w] : 0;
-            all += s_scan[1][w];
-        }
+    for (int i = w0; i < w1; i += 32) {
+        const uint32_t key = i + lane < w1 ? key_of(i + lane) : 0;
+        const bool in = i + lane < w1;
+        const unsigned bg = __ballot_sync(0xffffffffu, in && m > 0 && key > thr);
+        const unsigned be = __ballot_sync(0xffffffffu, in && m > 0 && key == thr);
+        const unsigned low = (1u << lane) - 1;
+        const int eq_before = eq + __popc(be & low);
+        const int before = gt + __popc(bg & low) + min(eq_before, left);
+        const bool keep = (bg >> lane & 1) || ((be >> lane & 1) && eq_before < left);
+        const int r = r0 + i + lane;
         if (keep) kept[before] = r;
-        if (gone && r < n && !keep) gone[r - before] = r;
-        base_eq += all_eq;
-        base_keep += all;
-        __syncthreads();
+        else if (in && gone) gone[r - before] = r;
+        gt += __popc(bg);
+        eq += __popc(be);
     }
+    if (CS > 1) cluster_sync();         // no CTA leaves while another reads its counts
 }
 
-// Copies the kept rows: one warp per (unit, row).
+// ---- move ---------------------------------------------------------------------------------------
+//
+// Copies the kept rows: 16 bytes per thread and row, four rows of keys and values in flight each.
+template <typename T, int D>
+struct MoveTile {
+    static constexpr int CPR = D * (int)sizeof(T) / 16, LINES = 256 / CPR, ROWS = 4 * LINES;
+};
+
 template <typename T, int D>
 __global__ void __launch_bounds__(256)
-k_evict_move(T *k_pages, T *v_pages, float *weights, PageArgs a, EvictArgs e, int64_t rows)
+k_evict_move(T *k_pages, T *v_pages, float *weights, PageArgs a, EvictArgs e, int blocks)
 {
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
-    if (i >= rows) return;
-    const int lane = threadIdx.x & 31, j = (int)(i % e.budget);
-    const int64_t unit = i / e.budget, b = unit / a.Hkv;
-    const int kvh = (int)(unit % a.Hkv), n = min(cached_rows(a, b), e.budget);
-    if (j >= n) return;
+    using Tile = MoveTile<T, D>;
+    constexpr int CPR = Tile::CPR, LINES = Tile::LINES, ROWS = Tile::ROWS;
+    __shared__ int64_t s_from[ROWS], s_to[ROWS];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t unit = blockIdx.x / blocks, b = unit / a.Hkv;
+    const int j0 = (int)(blockIdx.x % blocks) * ROWS;
+    const int kvh = (int)(unit % a.Hkv), n = min(cached_rows(a, b), e.budget), tid = threadIdx.x;
+    if (j0 >= n) return;
     PageArgs dst = a;
     dst.table = e.dst_table;
     dst.max_pages = e.dst_pages;
-    const int64_t from = pool_row(a, a.table + b * a.max_pages, e.kept[unit * e.budget + j], kvh);
-    const int64_t to = pool_row(dst, e.dst_table + b * e.dst_pages, j, kvh);
-    if (from < 0 || to < 0 || from == to) return;
-    for (int c = lane; c < D; c += 32) {
-        k_pages[to * D + c] = k_pages[from * D + c];
-        v_pages[to * D + c] = v_pages[from * D + c];
+    for (int i = tid; i < ROWS; i += 256) {
+        int64_t from = -1, to = -1;
+        if (j0 + i < n) {
+            from = pool_row(a, a.table + b * a.max_pages, e.kept[unit * e.budget + j0 + i], kvh);
+            to = pool_row(dst, e.dst_table + b * e.dst_pages, j0 + i, kvh);
+            if (from < 0 || to < 0 || from == to) from = -1;
+            else weights[to] = weights[from];
+        }
+        s_from[i] = from;
+        s_to[i] = to;
     }
-    if (lane == 0) weights[to] = weights[from];
+    __syncthreads();
+    const int c = tid % CPR, line = tid / CPR;
+    uint4 *kp = reinterpret_cast<uint4 *>(k_pages), *vp = reinterpret_cast<uint4 *>(v_pages);
+    uint4 x[4], y[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int64_t from = s_from[line + u * LINES];
+        if (from >= 0) {
+            x[u] = __ldcs(kp + from * CPR + c);
+            y[u] = __ldcs(vp + from * CPR + c);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int64_t to = s_to[line + u * LINES];
+        if (s_from[line + u * LINES] >= 0) {
+            kp[to * CPR + c] = x[u];
+            vp[to * CPR + c] = y[u];
+        }
+    }
 }
 
-// The evicted rows of one (batch, kv head) into its memory: one CTA, 32 rows at a time.
+// ---- fold ---------------------------------------------------------------------------------------
+//
+// sum sigma(k) v^T over a head's evicted rows, on tcgen05: A = sigma(K)^T (M = the key features),
+// B = V (N = the value features), both staged row by row (MN-major), 64 rows a step.  M and z are
+// 32-bit sums, so sigma(k) is split into three bf16 parts (24 bits; two would leave 2^-18, more
+// than the sum's own rounding), v into one (bf16, exact) or three (fp32: the six products down to
+// 2^-24 are kept).  The leading product has an accumulator of its own and every step's result is
+// read out and added in registers: the tensor core's own additions over a long axis lose about
+// one unit per addition, all in one direction.
+//
+// The evicted rows of all heads are shared out evenly over 148 CTAs (share.cuh).  In each, eight
+// loader warps keep a step of rows in flight in registers, form sigma and the parts and sum z;
+// one thread issues the products; eight warps read the accumulators.  Reading K and V is the
+// bound (4 d bytes a row against 2 d^2 operations); the parts' products are a quarter of the
+// tensor rate at that speed.
+constexpr int kFoldCtas = 148;
+constexpr int kFoldLoaders = 8, kFoldReaders = 8;
+constexpr int kFoldThreads = 32 * (kFoldLoaders + kFoldReaders + 1);
+constexpr int kFoldRows = 64;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(256)
-k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageArgs a, EvictArgs e,
-             float *M, float *z)
+struct FoldTile {
+    static constexpr bool kWide = sizeof(T) == 4;
+    static constexpr int VP = kWide ? 3 : 1;               // parts of v
+    static constexpr int KB = 2 * kFoldRows * 128;         // bytes of a part: two blocks of 64 columns
+    static constexpr int STAGE = (3 + VP) * KB;
+    static constexpr int STAGES = kWide ? 2 : 3;
+    static constexpr int SMEM = STAGES * STAGE + 1024;     // rounded up to 1024 inside
+    static constexpr int CPR = D * (int)sizeof(T) / 16;    // 16-byte chunks of a row
+    static constexpr int LD = kFoldRows / kFoldLoaders * CPR / 32;   // chunks per lane, tensor and step
+    static constexpr int E = 16 / (int)sizeof(T);          // channels of a chunk
+    static constexpr uint32_t COLS = 4 * D;                // two buffers of two accumulators
+};
+
+__device__ __forceinline__ float sigma_fast(float x)
 {
-    constexpr int TK = 32, R = D / 16;
-    __shared__ float sK[TK][D + 1];
-    __shared__ float sV[TK][D + 1];
-    const int64_t unit = blockIdx.x, b = unit / a.Hkv;
-    const int kvh = (int)(unit % a.Hkv), tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
-    const int count = cached_rows(a, b) - e.budget;
-    if (count <= 0) return;
-    const int *table = a.table + b * a.max_pages, *gone = e.gone + unit * e.gone_stride;
-    float acc[R][R], zacc = 0.f;
+    return x > 0.f ? x + 1.f : tc::ex2(x * 1.4426950408889634f);
+}
+
+// x = h + m + l in bf16 parts, to 2^-25 of it; pairs packed.
+__device__ __forceinline__ void split3(float x, float y, uint32_t (&p)[3])
+{
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int j = 0; j < R; ++j) acc[i][j] = 0.f;
-    for (int t0 = 0; t0 < count; t0 += TK) {
-        for (int i = tid; i < TK * D; i += 256) {
-            const int t = i / D, c = i % D;
-            const int64_t row = t0 + t < count ? pool_row(a, table, gone[t0 + t], kvh) : -1;
-            sK[t][c] = row >= 0 ? feature_map(ld_f(k_pages + row * D + c)) : 0.f;
-            sV[t][c] = row >= 0 ? ld_f(v_pages + row * D + c) : 0.f;
-        }
-        __syncthreads();
-        for (int t = 0; t < TK; ++t) {
-#pragma unroll
-            for (int i = 0; i < R; ++i)
-#pragma unroll
-                for (int j = 0; j < R; ++j)
-                    acc[i][j] = fmaf(sK[t][ty + 16 * i], sV[t][tx + 16 * j], acc[i][j]);
-        }
-        if (tid < D)
-            for (int t = 0; t < TK; ++t) zacc += sK[t][tid];
-        __syncthreads();
+    for (int i = 0; i < 3; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        p[i] = *reinterpret_cast<const uint32_t *>(&h);
+        x -= __uint_as_float(p[i] << 16);
+        y -= __uint_as_float(p[i] & 0xffff0000u);
     }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kFoldThreads, 1)
+k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageArgs a, EvictArgs e, float *M)
+{
+    using Tile = FoldTile<T, D>;
+    constexpr int CPR = Tile::CPR, LD = Tile::LD, E = Tile::E, ST = Tile::STAGES, VP = Tile::VP;
+    extern __shared__ unsigned char s_raw[];
+    __shared__ __align__(8) uint64_t full[ST], empty[ST], tfull[2], tempty[2];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    __shared__ ShareScratch s_share;
+    unsigned char *base = s_raw + ((1024 - (tc::smem_u32(s_raw) & 1023)) & 1023);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    auto rows_of = [&](int64_t b) { return (int64_t)max(0, cached_rows(a, b) - e.budget); };
+    Walk first;
+    int64_t t0, t1;
+    share_begin<kFoldCtas, kFoldThreads>(rows_of, e.B, a.Hkv, kFoldRows, s_share, t0, t1, first);
+    if (t0 >= t1) return;               // the whole CTA
+
+    if (tid == 0) {
+        for (int i = 0; i < ST; ++i) {
+            tc::mbar_init(&full[i], kFoldLoaders);
+            tc::mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&tfull[i], 1);
+            tc::mbar_init(&tempty[i], kFoldReaders);
+        }
+        s_abort = 0;
+        tc::fence_barrier_init();
+    }
+    if (D < 128)                        // columns that no row fills: features past D are 0
+        for (int i = tid; i < ST * Tile::STAGE / 16; i += kFoldThreads)
+            reinterpret_cast<uint4 *>(base)[i] = make_uint4(0, 0, 0, 0);
+    if (warp == 0) tc::tmem_alloc(&s_tmem, Tile::COLS);
+    tc::fence_proxy_async_smem();
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    volatile int *abort = &s_abort;
+    const int64_t steps = t1 - t0;
+
+    if (warp < kFoldLoaders) {
+        // a pipeline of its own for each step's addresses: the evicted row's number three steps
+        // ahead, its page two, its data one
+        Walk ahead = first;
+        int64_t t_ahead = t0;
+        int r1 = -1, kvh1 = 0, r2 = -1, kvh2 = 0, pg2 = -1;
+        int64_t b1 = 0, base3 = -1;
+        auto take_row = [&] {
+            r1 = -1;
+            if (t_ahead >= t1) return;
+            const int64_t j = ahead.tile * kFoldRows + warp * 8 + lane;
+            b1 = ahead.b;
+            kvh1 = ahead.kh;
+            if (lane < 8 && j < ahead.n) r1 = e.gone[(b1 * a.Hkv + kvh1) * e.gone_stride + j];
+            walk_next(ahead, rows_of, a.Hkv, e.B, kFoldRows);
+            ++t_ahead;
+        };
+        auto take_page = [&] {
+            r2 = r1;
+            kvh2 = kvh1;
+            pg2 = -1;
+            if (r2 >= 0) {
+                const int i = r2 >> a.shift;
+                pg2 = i < a.max_pages ? a.table[b1 * a.max_pages + i] : -1;
+            }
+        };
+        auto take_base = [&] {
+            base3 = -1;
+            if (r2 >= 0) {
+                if (pg2 >= 0 && pg2 < a.P)
+                    base3 = ((((int64_t)pg2 * a.Hkv + kvh2) << a.shift) | (r2 & ((1 << a.shift) - 1)));
+                else
+                    g_page_status = 1;
+            }
+        };
+        uint4 rk[LD], rv[LD];
+        bool ok[LD];
+        auto load = [&](int i) {
+            const int ci = i * 32 + lane;
+            const int64_t at = __shfl_sync(0xffffffffu, base3, ci / CPR);
+            ok[i] = at >= 0;
+            rk[i] = rv[i] = make_uint4(0, 0, 0, 0);
+            if (at >= 0) {
+                rk[i] = __ldcs(reinterpret_cast<const uint4 *>(k_pages) + at * CPR + ci % CPR);
+                rv[i] = __ldcs(reinterpret_cast<const uint4 *>(v_pages) + at * CPR + ci % CPR);
+            }
+        };
+        take_row();
+        take_page();
+        take_row();
+        take_base();
+        take_page();
+        take_row();
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+        for (int i = 0; i < LD; ++i) load(i);
+        // chunk ci of every step is the same column of this lane
+        float zs[E];
 #pragma unroll
-        for (int j = 0; j < R; ++j) M[unit * D * D + (ty + 16 * i) * D + tx + 16 * j] += acc[i][j];
-    if (tid < D) z[unit * D + tid] += zacc;
+        for (int x = 0; x < E; ++x) zs[x] = 0.f;
+        Walk at = first;
+        for (int64_t t = t0; t < t1; ++t) {
+            const int64_t s = t - t0;
+            const int stage = (int)(s % ST);
+            if (s >= ST && !tc::mbar_wait(&empty[stage], (uint32_t)((s / ST - 1) & 1), abort, 90)) break;
+            take_base();
+            take_page();
+            take_row();
+            unsigned char *sk = base + stage * Tile::STAGE, *sv = sk + 3 * Tile::KB;
+#pragma unroll
+            for (int i = 0; i < LD; ++i) {
+                const int ci = i * 32 + lane, r = warp * 8 + ci / CPR, ch = ci % CPR * E;   // row, first channel
+                // column block, then the row's swizzled 16-byte chunk of 8 channels
+                const uint32_t dst = (ch >> 6) * (kFoldRows * 128) + r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4) +
+                                     (ch & 7) * 2;
+                if constexpr (!Tile::kWide) {
+                    const uint32_t w[4] = {rk[i].x, rk[i].y, rk[i].z, rk[i].w};
+                    uint32_t p[4][3];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const float f0 = ok[i] ? sigma_fast(__uint_as_float(w[x] << 16)) : 0.f;
+                        const float f1 = ok[i] ? sigma_fast(__uint_as_float(w[x] & 0xffff0000u)) : 0.f;
+                        zs[2 * x] += f0;
+                        zs[2 * x + 1] += f1;
+                        split3(f0, f1, p[x]);
+                    }
+#pragma unroll
+                    for (int y = 0; y < 3; ++y)
+                        *reinterpret_cast<uint4 *>(sk + y * Tile::KB + dst) = make_uint4(p[0][y], p[1][y], p[2][y], p[3][y]);
+                    *reinterpret_cast<uint4 *>(sv + dst) = rv[i];
+                } else {
+                    const uint32_t w[4] = {rk[i].x, rk[i].y, rk[i].z, rk[i].w};
+                    uint32_t p[2][3], q[2][3];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float f0 = ok[i] ? sigma_fast(__uint_as_float(w[2 * x])) : 0.f;
+                        const float f1 = ok[i] ? sigma_fast(__uint_as_float(w[2 * x + 1])) : 0.f;
+                        zs[2 * x] += f0;
+                        zs[2 * x + 1] += f1;
+                        split3(f0, f1, p[x]);
+                    }
+                    split3(__uint_as_float(rv[i].x), __uint_as_float(rv[i].y), q[0]);
+                    split3(__uint_as_float(rv[i].z), __uint_as_float(rv[i].w), q[1]);
+#pragma unroll
+                    for (int y = 0; y < 3; ++y) {
+                        *reinterpret_cast<uint2 *>(sk + y * Tile::KB + dst) = make_uint2(p[0][y], p[1][y]);
+                        *reinterpret_cast<uint2 *>(sv + y * Tile::KB + dst) = make_uint2(q[0][y], q[1][y]);
+                    }
+                }
+                load(i);                // the next step's chunk into the registers just read
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&full[stage]);
+            if (t == t1 - 1 || at.tile == at.nt - 1) {   // a piece ends: this warp's part of z
+                const int64_t slot = blockIdx.x + at.b * a.Hkv + at.kh;
+#pragma unroll
+                for (int x = 0; x < E; ++x) {
+#pragma unroll
+                    for (int off = CPR; off < 32; off <<= 1) zs[x] += __shfl_xor_sync(0xffffffffu, zs[x], off);
+                    if (lane < CPR) e.part_z[(slot * kFoldLoaders + warp) * D + lane * E + x] = zs[x];
+                    zs[x] = 0.f;
+                }
+            }
+            walk_next(at, rows_of, a.Hkv, e.B, kFoldRows);
+        }
+    } else if (warp < kFoldLoaders + kFoldReaders) {
+        // reader w: lanes 32 (w % 4) .. + 31 (key features), half w / 4 of the columns
+        const int w = warp - kFoldLoaders, part = warp & 3, half = w >> 2, f = part * 32 + lane;
+        constexpr int NC = D / 2;       // columns of a half
+        float acc[NC];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) acc[i] = 0.f;
+        Walk at = first;
+        for (int64_t t = t0; t < t1; ++t) {
+            const int64_t s = t - t0;
+            const int buf = (int)(s & 1);
+            if (!tc::mbar_wait(&tfull[buf], (uint32_t)((s >> 1) & 1), abort, 91)) break;
+            tc::tc_fence_after();
+            if (part * 32 < D) {
+                const uint32_t col = tmem + ((uint32_t)(part * 32) << 16) + buf * 2 * D + half * NC;
+#pragma unroll
+                for (int c = 0; c < NC; c += 16) {
+                    uint32_t x[16], y[16];
+                    tc::tmem_ld16(col + c, x);
+                    tc::tmem_ld16(col + D + c, y);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[c + i] += __uint_as_float(x[i]) + __uint_as_float(y[i]);
+                }
+            }
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&tempty[buf]);
+            if (t == t1 - 1 || at.tile == at.nt - 1) {
+                if (part * 32 < D) {
+                    const int64_t unit = at.b * a.Hkv + at.kh;
+                    // a head that is this CTA's alone goes into its memory at once
+                    const bool whole = t - t0 >= at.nt - 1 && at.tile == at.nt - 1;
+                    float4 *dst = whole ? reinterpret_cast<float4 *>(M + unit * D * D + f * D + half * NC)
+                                        : reinterpret_cast<float4 *>(e.part_M + (blockIdx.x + unit) * D * D +
+                                                                     half * NC * D + f * 4);
+#pragma unroll
+                    for (int c = 0; c < NC; c += 4) {
+                        float4 x = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+                        float4 *p = dst + (whole ? c / 4 : c / 4 * D);   // pieces: [c / 4][f][4]
+                        if (whole) {
+                            const float4 y = *p;
+                            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                        }
+                        *p = x;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < NC; ++i) acc[i] = 0.f;
+            }
+            walk_next(at, rows_of, a.Hkv, e.B, kFoldRows);
+        }
+    } else if (lane == 0) {
+        constexpr uint32_t idesc = tc::idesc_bf16(128, D, 1, 1);
+        for (int64_t s = 0; s < steps; ++s) {
+            const int stage = (int)(s % ST), buf = (int)(s & 1);
+            if (s >= 2 && !tc::mbar_wait(&tempty[buf], (uint32_t)(((s >> 1) - 1) & 1), abort, 92)) break;
+            if (!tc::mbar_wait(&full[stage], (uint32_t)((s / ST) & 1), abort, 93)) break;
+            tc::tc_fence_after();
+            const uint32_t sk = tc::smem_u32(base + stage * Tile::STAGE), sv = sk + 3 * Tile::KB;
+            const uint32_t d0 = tmem + buf * 2 * D, d1 = d0 + D;
+            uint32_t on = 0;
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+#pragma unroll
+                for (int j = 0; j < VP; ++j) {
+                    if (i + j > 2) continue;
+                    for (int kk = 0; kk < kFoldRows / 16; ++kk) {
+                        const uint64_t da = tc::sdesc_sw128(sk + i * Tile::KB + kk * 2048, kFoldRows * 128, 1024);
+                        const uint64_t db = tc::sdesc_sw128(sv + j * Tile::KB + kk * 2048, kFoldRows * 128, 1024);
+                        if (i + j == 0) {
+                            tc::mma_ss(d0, da, db, idesc, kk > 0);
+                        } else {
+                            tc::mma_ss(d1, da, db, idesc, on);
+                            on = 1;
+                        }
+                    }
+                }
+            tc::mma_commit(&empty[stage]);
+            tc::mma_commit(&tfull[buf]);
+        }
+        // the last products end before TMEM is given back
+        for (int64_t s = steps > 2 ? steps - 2 : 0; s < steps; ++s)
+            tc::mbar_wait(&tfull[s & 1], (uint32_t)((s >> 1) & 1), abort, 94);
+    }
+    __syncwarp();
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    if (warp == 0) tc::tmem_dealloc(tmem, Tile::COLS);
+}
+
+// The pieces of a head that several CTAs folded, in order, into its memory; z of every head.
+template <int D>
+__global__ void __launch_bounds__(256)
+k_evict_reduce(PageArgs a, EvictArgs e, float *M, float *z)
+{
+    __shared__ ShareScratch s_share;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t unit = blockIdx.x, b = unit / a.Hkv;
+    const int kvh = (int)(unit % a.Hkv);
+    auto rows_of = [&](int64_t i) { return (int64_t)max(0, cached_rows(a, i) - e.budget); };
+    const int64_t n = rows_of(b), nt = (n + kFoldRows - 1) / kFoldRows;
+    if (n == 0) return;
+    int64_t before;
+    const int64_t total = a.Hkv * share_count<256>(rows_of, e.B, kFoldRows, b, s_share, before);
+    const int64_t s = before * a.Hkv + kvh * nt;
+    const int64_t c0 = share_owner<kFoldCtas>(s, total), c1 = share_owner<kFoldCtas>(s + nt - 1, total);
+    if (c0 != c1) {
+        const int i = blockIdx.y * 256 + threadIdx.x;      // [c / 4][f]
+        const int f = i % D, c4 = i / D;
+        const float4 *p = reinterpret_cast<const float4 *>(e.part_M);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int64_t c = c0; c <= c1; ++c) {
+            const float4 y = p[(c + unit) * (D * D / 4) + i];
+            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+        }
+        float4 *dst = reinterpret_cast<float4 *>(M) + (unit * D + f) * (D / 4) + c4;
+        const float4 y = *dst;
+        *dst = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+    }
+    if (blockIdx.y == 0 && threadIdx.x < D) {
+        float x = 0.f;
+        for (int64_t c = c0; c <= c1; ++c) {
+            const float *p = e.part_z + (c + unit) * kFoldLoaders * D + threadIdx.x;
+            float y = 0.f;
+#pragma unroll
+            for (int w = 0; w < kFoldLoaders; ++w) y += p[w * D];
+            x += y;
+        }
+        z[unit * D + threadIdx.x] += x;
+    }
 }
 
 }  // namespace paged

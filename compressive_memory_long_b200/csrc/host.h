@@ -18,8 +18,8 @@ private:
     void *rec_ = nullptr;
 };
 
-// Reads and clears the current device's record of bad page numbers: 0 none, 1 some, -1 if
-// the copy failed.
-int take_page_status();
+// Reads and clears the current device's records of the paged entries: a bounded wait that gave
+// up, and page numbers or rows outside a cache.  INFINI_OK, or INFINI_ERR_CUDA if a copy failed.
+int take_paged_status(bool &waits, bool &pages);
 
 }  // namespace infini

@@ -17,13 +17,19 @@
 
 namespace infini {
 
-int take_page_status()
+int take_paged_status(bool &waits, bool &pages)
 {
-    int v = 0;
+    int v[2] = {0, 0};
     const int zero = 0;
-    if (cudaMemcpyFromSymbol(&v, paged::g_page_status, sizeof(int)) != cudaSuccess) return -1;
-    if (v != 0 && cudaMemcpyToSymbol(paged::g_page_status, &zero, sizeof(int)) != cudaSuccess) return -1;
-    return v != 0;
+    if (cudaMemcpyFromSymbol(&v[0], tc::g_wait_status, sizeof(int)) != cudaSuccess ||
+        cudaMemcpyFromSymbol(&v[1], paged::g_page_status, sizeof(int)) != cudaSuccess)
+        return INFINI_ERR_CUDA;
+    if ((v[0] != 0 && cudaMemcpyToSymbol(tc::g_wait_status, &zero, sizeof(int)) != cudaSuccess) ||
+        (v[1] != 0 && cudaMemcpyToSymbol(paged::g_page_status, &zero, sizeof(int)) != cudaSuccess))
+        return INFINI_ERR_CUDA;
+    waits = v[0] != 0;
+    pages = v[1] != 0;
+    return INFINI_OK;
 }
 
 namespace {
@@ -92,11 +98,12 @@ bool opt_in_smem(size_t bytes)
 // Launches a kernel that may start while the one before it on the stream still runs (it waits
 // for that one's end itself).
 template <typename... P, typename... A>
-cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t st, A... args)
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -256,7 +263,7 @@ int launch_decode(const T *q, const T *k, const T *v, T *kp, T *vp, float *weigh
     int64_t chunks = 1;
     if (weights)   // enough CTAs for every SM several times over; a chunk takes more rows then
         chunks = std::max<int64_t>(1, std::min((most_rows + kJoinRows - 1) / kJoinRows, 2368 / units));
-    return launched(launch_early(k_paged_join<T, D>, dim3((unsigned)units, (unsigned)chunks), kJoinThreads, st, q,
+    return launched(launch_early(k_paged_join<T, D>, dim3((unsigned)units, (unsigned)chunks), kJoinThreads, 0, st, q,
                                  weights, out, a, dc, k ? 1 : 0));
 }
 
@@ -336,30 +343,67 @@ int paged_decode_step(const void *q, const void *k, const void *v, void *k_pages
     }
 }
 
-// The evicted rows of every (batch, kv head), when they go into a memory.
-int64_t evict_workspace_bytes(int64_t B, int64_t Hkv, int64_t page, int64_t max_pages, int64_t budget,
-                              int with_memory)
+// The evicted rows of every (batch, kv head), when they go into a memory, and the pieces of
+// their sums.
+struct EvictSpace {
+    int64_t gone, part_M, part_z, bytes;   // offsets of 4-byte words; bytes of all
+};
+
+EvictSpace evict_space(int64_t B, int64_t Hkv, int64_t d, int64_t page, int64_t max_pages, int64_t budget,
+                       int with_memory)
 {
+    EvictSpace s{0, 0, 0, 0};
     const int64_t most = max_pages * page - budget;
-    return with_memory && most > 0 ? B * Hkv * most * 4 : 0;
+    if (!with_memory || most <= 0) return s;
+    const int64_t slots = kFoldCtas + B * Hkv;
+    s.part_M = (B * Hkv * most + 3) / 4 * 4;
+    s.part_z = s.part_M + slots * d * d;
+    s.bytes = (s.part_z + slots * kFoldLoaders * d) * 4;
+    return s;
 }
 
 template <typename T, int D>
 int launch_evict(T *kp, T *vp, float *weights, const PageArgs &a, const EvictArgs &e, float *M, float *z,
-                 int64_t units, cudaStream_t st)
+                 int64_t units, int64_t most_rows, cudaStream_t st)
 {
+    // a cluster while that gives no more CTAs than SMs and each has 2048 rows at the least
+    int CS = 1;
+    while (CS < 8 && units * CS * 2 <= 148 && most_rows >= 2048 * 2 * CS) CS *= 2;
+    const int cap = (int)std::min<int64_t>((most_rows + CS - 1) / CS, kSelectKeys);
     {
         TraceScope trace("evict_select", st);
-        k_evict_select<<<(unsigned)units, 1024, 0, st>>>(weights, a, e);
+        if (!opt_in_smem<k_evict_select>((3 * kBins + kSelectKeys) * 4)) return INFINI_ERR_CUDA;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(units * CS));
+        cfg.blockDim = dim3(kSelectThreads);
+        cfg.dynamicSmemBytes = (size_t)(3 * kBins + cap) * 4;
+        cfg.stream = st;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = (unsigned)CS;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        const int rc = launched(cudaLaunchKernelEx(&cfg, k_evict_select, (const float *)weights, a, e, CS, cap));
+        if (rc != INFINI_OK) return rc;
     }
     if (M && e.gone) {
-        TraceScope trace("evict_fold", st);
-        k_evict_fold<T, D><<<(unsigned)units, 256, 0, st>>>(kp, vp, a, e, M, z);
+        if (!opt_in_smem<k_evict_fold<T, D>>(FoldTile<T, D>::SMEM)) return INFINI_ERR_CUDA;
+        {
+            TraceScope trace("evict_fold", st);
+            const int rc = launched(launch_early(k_evict_fold<T, D>, dim3(kFoldCtas), kFoldThreads,
+                                                 FoldTile<T, D>::SMEM, st, kp, vp, a, e, M));
+            if (rc != INFINI_OK) return rc;
+        }
+        TraceScope trace("evict_reduce", st);
+        const int rc = launched(launch_early(k_evict_reduce<D>, dim3((unsigned)units, (D * D / 4 + 255) / 256), 256, 0,
+                                             st, a, e, M, z));
+        if (rc != INFINI_OK) return rc;
     }
     TraceScope trace("evict_move", st);
-    k_evict_move<T, D><<<(unsigned)((units * e.budget + 7) / 8), 256, 0, st>>>(kp, vp, weights, a, e,
-                                                                                  units * e.budget);
-    return launched();
+    const int blocks = (e.budget + MoveTile<T, D>::ROWS - 1) / MoveTile<T, D>::ROWS;
+    return launched(launch_early(k_evict_move<T, D>, dim3((unsigned)(units * blocks)), 256, 0, st, kp, vp, weights, a,
+                                 e, blocks));
 }
 
 template <typename T>
@@ -378,10 +422,11 @@ int paged_evict(void *k_pages, void *v_pages, float *weights, const int *table, 
     if (rc == INFINI_ERR_INVALID_ARG) return rc;
     if (d <= 0 || budget <= 0 || recent < 0 || recent > budget || dst_pages <= 0 ||
         dst_pages > ((int64_t)1 << 31) - 1 || dst_pages * page < budget ||
-        B * Hkv * budget > ((int64_t)1 << 33))
+        budget > ((int64_t)1 << 30) || B * Hkv * budget > ((int64_t)1 << 33))
         return INFINI_ERR_INVALID_ARG;
     const int64_t es = (int64_t)sizeof(T), pool = P * Hkv * page, units = B * Hkv;
-    const int64_t need = evict_workspace_bytes(B, Hkv, page, max_pages, budget, M != nullptr);
+    const EvictSpace space = evict_space(B, Hkv, d, page, max_pages, budget, M != nullptr);
+    const int64_t need = space.bytes;
     if (workspace_bytes < need || (need > 0 && !workspace)) return INFINI_ERR_INVALID_ARG;
     for (const void *p : {(const void *)k_pages, (const void *)v_pages, (const void *)weights,
                           (const void *)M, (const void *)z, (const void *)workspace, (const void *)kept})
@@ -396,15 +441,28 @@ int paged_evict(void *k_pages, void *v_pages, float *weights, const int *table, 
         return INFINI_ERR_INVALID_ARG;
     if (rc != INFINI_OK || !head_dim(d)) return INFINI_ERR_UNSUPPORTED;
     if (M && rule == INFINI_UPDATE_DELTA) return INFINI_ERR_UNSUPPORTED;
-    const EvictArgs e{dst_table, (int)dst_pages, (int)budget, (int)recent, lens_out, kept,
-                      need > 0 ? static_cast<int *>(workspace) : nullptr, max_pages * page - budget};
+    float *ws = static_cast<float *>(workspace);
+    EvictArgs e{};
+    e.dst_table = dst_table;
+    e.dst_pages = (int)dst_pages;
+    e.budget = (int)budget;
+    e.recent = (int)recent;
+    e.lens_out = lens_out;
+    e.kept = kept;
+    e.B = B;
+    e.gone_stride = max_pages * page - budget;
+    if (need > 0) {
+        e.gone = reinterpret_cast<int *>(ws);
+        e.part_M = ws + space.part_M;
+        e.part_z = ws + space.part_z;
+    }
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaGetLastError();
     T *kp = static_cast<T *>(k_pages), *vp = static_cast<T *>(v_pages);
     switch (d) {
-    case 32: return launch_evict<T, 32>(kp, vp, weights, a, e, M, z, units, st);
-    case 64: return launch_evict<T, 64>(kp, vp, weights, a, e, M, z, units, st);
-    default: return launch_evict<T, 128>(kp, vp, weights, a, e, M, z, units, st);
+    case 32: return launch_evict<T, 32>(kp, vp, weights, a, e, M, z, units, max_pages * page, st);
+    case 64: return launch_evict<T, 64>(kp, vp, weights, a, e, M, z, units, max_pages * page, st);
+    default: return launch_evict<T, 128>(kp, vp, weights, a, e, M, z, units, max_pages * page, st);
     }
 }
 
@@ -488,7 +546,7 @@ int64_t infini_attn_paged_evict_workspace_bytes(int64_t B, int64_t Hkv, int64_t 
                                                 int64_t max_pages, int64_t budget, int with_memory)
 {
     if (B <= 0 || Hkv <= 0 || d <= 0 || page <= 0 || max_pages <= 0 || budget <= 0) return 0;
-    return infini::evict_workspace_bytes(B, Hkv, page, max_pages, budget, with_memory);
+    return infini::evict_space(B, Hkv, d, page, max_pages, budget, with_memory).bytes;
 }
 
 }  // extern "C"

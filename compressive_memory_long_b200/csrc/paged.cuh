@@ -3,7 +3,7 @@
 // The pool holds P pages of `page` rows for every key/value head, [P, Hkv, page, d]; row r of
 // sequence b lies in page table[b][r / page] at slot r % page.  A page number outside [0, P)
 // or a row past the table is never followed: the row is skipped and the device's page record
-// is set (take_page_status).
+// is set (infini_attn_device_status).
 #pragma once
 
 #include <cuda_bf16.h>
