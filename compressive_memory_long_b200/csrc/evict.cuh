@@ -209,15 +209,10 @@ k_evict_select(const float *__restrict__ weights, PageArgs a, EvictArgs e, int C
 //
 // Copies the kept rows: 16 bytes per thread and row, four rows of keys and values in flight each.
 template <typename T, int D>
-struct MoveTile {
-    static constexpr int CPR = D * (int)sizeof(T) / 16, LINES = 256 / CPR, ROWS = 4 * LINES;
-};
-
-template <typename T, int D>
 __global__ void __launch_bounds__(256)
 k_evict_move(T *k_pages, T *v_pages, float *weights, PageArgs a, EvictArgs e, int blocks)
 {
-    using Tile = MoveTile<T, D>;
+    using Tile = RowTile<T, D>;
     constexpr int CPR = Tile::CPR, LINES = Tile::LINES, ROWS = Tile::ROWS;
     __shared__ int64_t s_from[ROWS], s_to[ROWS];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -115,6 +115,34 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t sm
 
 // ---- rotary positions ---------------------------------------------------------------------
 
+bool row_aligned(const void *p, const int64_t s[3], int64_t es)
+{
+    return aligned(p, 16) && s[0] * es % 16 == 0 && s[1] * es % 16 == 0 && s[2] * es % 16 == 0;
+}
+
+template <typename T, int D>
+int launch_rotary(const T *q, const T *k, T *q_out, T *k_out, const RotaryArgs &a, int64_t B, bool rows, bool apart,
+                  cudaStream_t st)
+{
+    TraceScope trace("rotary", st);
+    constexpr int N = Vec<T>::N, U = D / (2 * N);
+    const bool even = a.interleaved || a.rot / 2 % N == 0;
+    if (!rows || !(even || apart)) {
+        const int64_t n = B * a.L * (D / 2);
+        k_rotary_pairs<T, D><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(q, k, q_out, k_out, a, n);
+        return launched();
+    }
+    // a thread takes all heads of its token, or fewer, so that the card has threads enough
+    const int64_t n = B * a.L * U, heads = a.H + a.Hkv;
+    const int64_t groups = std::max<int64_t>(1, std::min((heads + 3) / 4, ((int64_t)148 * 2048 + n - 1) / n));
+    const int per = (int)((heads + groups - 1) / groups);
+    const dim3 grid((unsigned)((n + 255) / 256), (unsigned)((heads + per - 1) / per));
+    if (a.interleaved) k_rotary_rows<T, D, kPairs><<<grid, 256, 0, st>>>(q, k, q_out, k_out, a, n, per);
+    else if (even) k_rotary_rows<T, D, kHalves><<<grid, 256, 0, st>>>(q, k, q_out, k_out, a, n, per);
+    else k_rotary_rows<T, D, kRagged><<<grid, 256, 0, st>>>(q, k, q_out, k_out, a, n, per);
+    return launched();
+}
+
 template <typename T>
 int rotary(const void *q, const void *k, void *q_out, void *k_out, const double *freq,
            const int64_t *positions, int64_t start, const int64_t *q_strides,
@@ -162,15 +190,13 @@ int rotary(const void *q, const void *k, void *q_out, void *k_out, const double 
     cudaGetLastError();
     const T *tq = static_cast<const T *>(q), *tk = static_cast<const T *>(k);
     T *oq = static_cast<T *>(q_out), *ok = static_cast<T *>(k_out);
-    TraceScope trace("rotary", st);
-    const int64_t n = B * L * (d / 2);
-    const unsigned grid = (unsigned)((n + 255) / 256);
+    const bool apart = !q_in && !k_in;
+    const bool rows = row_aligned(q, a.sq, es) && (!k || row_aligned(k, a.sk, es));
     switch (d) {
-    case 32: k_rotary<T, 32><<<grid, 256, 0, st>>>(tq, tk, oq, ok, a, n); break;
-    case 64: k_rotary<T, 64><<<grid, 256, 0, st>>>(tq, tk, oq, ok, a, n); break;
-    default: k_rotary<T, 128><<<grid, 256, 0, st>>>(tq, tk, oq, ok, a, n); break;
+    case 32: return launch_rotary<T, 32>(tq, tk, oq, ok, a, B, rows, apart, st);
+    case 64: return launch_rotary<T, 64>(tq, tk, oq, ok, a, B, rows, apart, st);
+    default: return launch_rotary<T, 128>(tq, tk, oq, ok, a, B, rows, apart, st);
     }
-    return launched();
 }
 
 // ---- the paged cache ------------------------------------------------------------------------
@@ -219,15 +245,18 @@ int paged_append(const void *k, const void *v, const int64_t *k_strides, const i
     const T *tk = static_cast<const T *>(k), *tv = static_cast<const T *>(v);
     T *kp = static_cast<T *>(k_pages), *vp = static_cast<T *>(v_pages);
     TraceScope trace("paged_append", st);
-    const int64_t n = B * Hkv * Tn * d;
-    const unsigned grid = (unsigned)((n + 255) / 256);
-#define APPEND(D)                                                                                  \
-    k_paged_append<T, D><<<grid, 256, 0, st>>>(tk, tv, kp, vp, weights, a, counts, sk[0], sk[1], sk[2], \
-                                               sv[0], sv[1], sv[2], Tn, n)
+    const bool rows = row_aligned(k, sk, es) && row_aligned(v, sv, es);
+#define APPEND(D, ALIGNED)                                                                          \
+    do {                                                                                            \
+        const int64_t blocks = (Tn * Hkv + RowTile<T, D>::ROWS - 1) / RowTile<T, D>::ROWS;          \
+        if (B * blocks > ((int64_t)1 << 31) - 1) return INFINI_ERR_INVALID_ARG;                     \
+        k_paged_append<T, D, ALIGNED><<<(unsigned)(B * blocks), 256, 0, st>>>(                      \
+            tk, tv, kp, vp, weights, a, counts, sk[0], sk[1], sk[2], sv[0], sv[1], sv[2], Tn, blocks); \
+    } while (0)
     switch (d) {
-    case 32: APPEND(32); break;
-    case 64: APPEND(64); break;
-    default: APPEND(128); break;
+    case 32: if (rows) APPEND(32, true); else APPEND(32, false); break;
+    case 64: if (rows) APPEND(64, true); else APPEND(64, false); break;
+    default: if (rows) APPEND(128, true); else APPEND(128, false); break;
     }
 #undef APPEND
     return launched();
@@ -401,7 +430,7 @@ int launch_evict(T *kp, T *vp, float *weights, const PageArgs &a, const EvictArg
         if (rc != INFINI_OK) return rc;
     }
     TraceScope trace("evict_move", st);
-    const int blocks = (e.budget + MoveTile<T, D>::ROWS - 1) / MoveTile<T, D>::ROWS;
+    const int blocks = (e.budget + RowTile<T, D>::ROWS - 1) / RowTile<T, D>::ROWS;
     return launched(launch_early(k_evict_move<T, D>, dim3((unsigned)(units * blocks)), 256, 0, st, kp, vp, weights, a,
                                  e, blocks));
 }

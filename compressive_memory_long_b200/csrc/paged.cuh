@@ -45,25 +45,70 @@ __device__ __forceinline__ int64_t pool_row(const PageArgs &a, const int *table_
     return ((((int64_t)pg * a.Hkv + kvh) << a.shift) | (r & (((int64_t)1 << a.shift) - 1)));
 }
 
-// Rows lens[b] .. lens[b] + counts[b] - 1 of the pages from k / v [B, Hkv, T, d] (strided);
-// their accumulated weights start at 0.  One thread per element.
+// A block's rows when 16 bytes go to a thread and row: four rows of keys and values in flight.
 template <typename T, int D>
+struct RowTile {
+    static constexpr int CPR = D * (int)sizeof(T) / 16, LINES = 256 / CPR, ROWS = 4 * LINES;
+};
+
+// Chunk c of a row, whose address needs an element's alignment only when !ALIGNED.
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ uint4 load_chunk(const T *row, int c)
+{
+    if constexpr (ALIGNED) {
+        return __ldcs(reinterpret_cast<const uint4 *>(row) + c);
+    } else {
+        constexpr int E = 16 / (int)sizeof(T);
+        union {
+            uint4 v;
+            T x[E];
+        } u;
+#pragma unroll
+        for (int i = 0; i < E; ++i) u.x[i] = row[c * E + i];
+        return u.v;
+    }
+}
+
+// Rows lens[b] .. lens[b] + counts[b] - 1 of the pages from k / v [B, Hkv, T, d] (strided);
+// their accumulated weights start at 0.  A copy: bandwidth is the bound, and for one token a
+// sequence the latency of lens, table and row one after the other.  A block takes ROWS (token,
+// head) rows of one sequence, heads first (a token-major projection is read in one run); those
+// past a sequence's count return at once.
+template <typename T, int D, bool ALIGNED>
 __global__ void __launch_bounds__(256)
 k_paged_append(const T *__restrict__ k, const T *__restrict__ v, T *k_pages, T *v_pages,
                float *weights, PageArgs a, const int *__restrict__ counts, int64_t sk0, int64_t sk1,
-               int64_t sk2, int64_t sv0, int64_t sv1, int64_t sv2, int64_t Tn, int64_t n)
+               int64_t sk2, int64_t sv0, int64_t sv1, int64_t sv2, int64_t Tn, int64_t blocks)
 {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n) return;
-    const int c = (int)(i % D);
-    const int64_t t = i / D % Tn, bh = i / D / Tn, b = bh / a.Hkv;
-    const int kvh = (int)(bh % a.Hkv), len = cached_rows(a, b);
-    if (len < 0 || t >= (counts ? (int64_t)counts[b] : Tn)) return;
-    const int64_t row = pool_row(a, a.table + b * a.max_pages, len + t, kvh);
-    if (row < 0) return;
-    k_pages[row * D + c] = k[b * sk0 + kvh * sk1 + t * sk2 + c];
-    v_pages[row * D + c] = v[b * sv0 + kvh * sv1 + t * sv2 + c];
-    if (weights && c == 0) weights[row] = 0.f;
+    using Tile = RowTile<T, D>;
+    constexpr int CPR = Tile::CPR, LINES = Tile::LINES;
+    const int64_t b = blockIdx.x / blocks, i0 = blockIdx.x % blocks * Tile::ROWS;
+    const int len = cached_rows(a, b);
+    const int64_t n = (counts ? min((int64_t)max(counts[b], 0), Tn) : Tn) * a.Hkv;
+    if (len < 0 || i0 >= n) return;
+    const int c = threadIdx.x % CPR, line = threadIdx.x / CPR;
+    uint4 *kp = reinterpret_cast<uint4 *>(k_pages), *vp = reinterpret_cast<uint4 *>(v_pages);
+    uint4 x[4], y[4];
+    int64_t row[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int64_t i = i0 + line + u * LINES;
+        row[u] = -1;
+        if (i < n) {
+            const int64_t t = i / a.Hkv;
+            const int kvh = (int)(i % a.Hkv);
+            x[u] = load_chunk<T, ALIGNED>(k + b * sk0 + kvh * sk1 + t * sk2, c);
+            y[u] = load_chunk<T, ALIGNED>(v + b * sv0 + kvh * sv1 + t * sv2, c);
+            row[u] = pool_row(a, a.table + b * a.max_pages, len + t, kvh);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        if (row[u] >= 0) {
+            kp[row[u] * CPR + c] = x[u];
+            vp[row[u] * CPR + c] = y[u];
+            if (weights && c == 0) weights[row[u]] = 0.f;
+        }
 }
 
 }  // namespace paged

@@ -42,41 +42,182 @@ __device__ __forceinline__ float2 rotary_turn(double pos, double freq, float sca
     return make_float2(c * scale, s * scale);
 }
 
-// One thread per (batch, token, pair or pair of copied channels); it forms the turn once and
-// applies it to every head.
+// The turn of pair i at this thread's position.
+__device__ __forceinline__ float2 turn_of(const RotaryArgs &a, int64_t bt, int64_t t, int i)
+{
+    const double pos = (double)(a.positions ? a.positions[bt] : a.start + t);
+    float2 cs = rotary_turn(pos, a.freq[i], a.scale);
+    if (a.backward) cs.y = -cs.y;
+    return cs;
+}
+
+template <typename T>
+__device__ __forceinline__ const T *rotary_in(const T *q, const T *k, const RotaryArgs &a, int64_t b, int64_t t, int h)
+{
+    return h < a.H ? q + b * a.sq[0] + h * a.sq[1] + t * a.sq[2]
+                   : k + b * a.sk[0] + (h - a.H) * a.sk[1] + t * a.sk[2];
+}
+
+template <typename T, int D>
+__device__ __forceinline__ T *rotary_out(T *q_out, T *k_out, const RotaryArgs &a, int64_t b, int64_t t, int h)
+{
+    return h < a.H ? q_out + ((b * a.H + h) * a.L + t) * D : k_out + ((b * a.Hkv + h - a.H) * a.L + t) * D;
+}
+
+// 16 bytes of a row as 32-bit values, and back.
+template <typename T>
+struct Vec {
+    static constexpr int N = 16 / (int)sizeof(T);
+    static __device__ __forceinline__ void get(const uint4 &v, float (&x)[N])
+    {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 2) {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            } else {
+                x[i] = __uint_as_float(w[i]);
+            }
+        }
+    }
+    static __device__ __forceinline__ uint4 put(const float (&x)[N])
+    {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 2) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            } else {
+                w[i] = __float_as_uint(x[i]);
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// Bandwidth is the bound: every element is read and written once.  A thread owns two 16-byte
+// vectors of a token's row and applies its turns, formed once, to its heads, four heads' loads
+// in flight at a time.  The vectors are
+//   kHalves:  channels c and c + rot/2 (rot/2 a whole number of vectors), or two copied ones;
+//   kPairs:   neighbours, each holding whole pairs (interleaved);
+//   kRagged:  neighbours, partners read one by one (rot/2 cuts a vector; not in place, where a
+//             partner may have been written already).
+enum RotaryForm { kHalves, kPairs, kRagged };
+
+template <typename T, int D, int FORM>
+__global__ void __launch_bounds__(256)
+k_rotary_rows(const T *q, const T *k, T *q_out, T *k_out, RotaryArgs a, int64_t n, int per)
+{
+    constexpr int N = Vec<T>::N, U = D / (2 * N), NB = 4, NC = FORM == kRagged ? 2 * N : N;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    const int u = (int)(i % U), half = a.rot / 2;
+    const int64_t bt = i / U, b = bt / a.L, t = bt % a.L;
+    int c1 = 2 * u * N, c2 = c1 + N;
+    bool turned = c1 < a.rot;
+    if (FORM == kHalves) {
+        turned = u < half / N;
+        c1 = turned ? u * N : a.rot + 2 * (u - half / N) * N;
+        c2 = turned ? c1 + half : c1 + N;
+    }
+    float2 cs[NC];
+#pragma unroll
+    for (int e = 0; e < NC; ++e) {
+        cs[e] = make_float2(1.f, 0.f);
+        if (FORM == kHalves) {
+            if (turned) cs[e] = turn_of(a, bt, t, c1 + e);
+        } else if (FORM == kPairs) {
+            if (c1 + 2 * e < a.rot) cs[e] = turn_of(a, bt, t, c1 / 2 + e);
+        } else if (c1 + e < a.rot) {
+            cs[e] = turn_of(a, bt, t, c1 + e < half ? c1 + e : c1 + e - half);
+            if (c1 + e < half) cs[e].y = -cs[e].y;         // y = x cos + partner * (+-sin)
+        }
+    }
+    const int h1 = min(((int)blockIdx.y + 1) * per, a.H + a.Hkv);
+    for (int h0 = blockIdx.y * per; h0 < h1; h0 += NB) {
+        uint4 v[NB][2];
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            if (h0 + j < h1) {
+                const T *x = rotary_in(q, k, a, b, t, h0 + j);
+                v[j][0] = *reinterpret_cast<const uint4 *>(x + c1);
+                v[j][1] = *reinterpret_cast<const uint4 *>(x + c2);
+            }
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            if (h0 + j < h1) {
+                if (turned) {
+                    float x1[N], x2[N], y1[N], y2[N];
+                    Vec<T>::get(v[j][0], x1);
+                    Vec<T>::get(v[j][1], x2);
+                    if (FORM == kHalves) {
+#pragma unroll
+                        for (int e = 0; e < N; ++e) {
+                            y1[e] = x1[e] * cs[e].x - x2[e] * cs[e].y;
+                            y2[e] = x2[e] * cs[e].x + x1[e] * cs[e].y;
+                        }
+                    } else if (FORM == kPairs) {
+#pragma unroll
+                        for (int e = 0; e < N / 2; ++e) {
+                            const float2 w1 = cs[e], w2 = cs[(e + N / 2) % NC];
+                            const bool on1 = c1 + 2 * e < a.rot, on2 = c2 + 2 * e < a.rot;
+                            y1[2 * e] = on1 ? x1[2 * e] * w1.x - x1[2 * e + 1] * w1.y : x1[2 * e];
+                            y1[2 * e + 1] = on1 ? x1[2 * e + 1] * w1.x + x1[2 * e] * w1.y : x1[2 * e + 1];
+                            y2[2 * e] = on2 ? x2[2 * e] * w2.x - x2[2 * e + 1] * w2.y : x2[2 * e];
+                            y2[2 * e + 1] = on2 ? x2[2 * e + 1] * w2.x + x2[2 * e] * w2.y : x2[2 * e + 1];
+                        }
+                    } else {
+                        const T *x = rotary_in(q, k, a, b, t, h0 + j);
+                        auto turn = [&](float y, int c, float2 w) {
+                            return c < a.rot ? y * w.x + ld_f(x + (c < half ? c + half : c - half)) * w.y : y;
+                        };
+#pragma unroll
+                        for (int e = 0; e < N; ++e) {
+                            y1[e] = turn(x1[e], c1 + e, cs[e]);
+                            y2[e] = turn(x2[e], c2 + e, cs[(e + N) % NC]);
+                        }
+                    }
+                    v[j][0] = Vec<T>::put(y1);
+                    v[j][1] = FORM != kHalves && c2 >= a.rot ? v[j][1] : Vec<T>::put(y2);
+                }
+                T *y = rotary_out<T, D>(q_out, k_out, a, b, t, h0 + j);
+                *reinterpret_cast<uint4 *>(y + c1) = v[j][0];
+                *reinterpret_cast<uint4 *>(y + c2) = v[j][1];
+            }
+    }
+}
+
+// Rows off 16-byte boundaries, and ragged halves in place: one thread per (batch, token, pair or
+// pair of copied channels), which alone reads and writes that pair in every head.
 template <typename T, int D>
 __global__ void __launch_bounds__(256)
-k_rotary(const T *q, const T *k, T *q_out, T *k_out, RotaryArgs a, int64_t n)
+k_rotary_pairs(const T *q, const T *k, T *q_out, T *k_out, RotaryArgs a, int64_t n)
 {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n) return;
     const int u = (int)(i % (D / 2));
     const int64_t bt = i / (D / 2), b = bt / a.L, t = bt % a.L;
-    int c1, c2;
+    int c1 = 2 * u, c2 = 2 * u + 1;
     float2 cs = make_float2(1.f, 0.f);
     if (u < a.rot / 2) {
-        c1 = a.interleaved ? 2 * u : u;
-        c2 = a.interleaved ? 2 * u + 1 : u + a.rot / 2;
-        const double pos = (double)(a.positions ? a.positions[bt] : a.start + t);
-        cs = rotary_turn(pos, a.freq[u], a.scale);
-        if (a.backward) cs.y = -cs.y;
-    } else {
-        c1 = 2 * u;
-        c2 = 2 * u + 1;
+        if (!a.interleaved) {
+            c1 = u;
+            c2 = u + a.rot / 2;
+        }
+        cs = turn_of(a, bt, t, u);
     }
     for (int h = 0; h < a.H + a.Hkv; ++h) {
-        const bool isq = h < a.H;
-        const int hh = isq ? h : h - a.H;
-        const T *x = isq ? q + b * a.sq[0] + hh * a.sq[1] + t * a.sq[2]
-                         : k + b * a.sk[0] + hh * a.sk[1] + t * a.sk[2];
-        T *y = isq ? q_out + ((b * a.H + hh) * a.L + t) * D : k_out + ((b * a.Hkv + hh) * a.L + t) * D;
+        const T *x = rotary_in(q, k, a, b, t, h);
+        T *y = rotary_out<T, D>(q_out, k_out, a, b, t, h);
+        const T v1 = x[c1], v2 = x[c2];
         if (u >= a.rot / 2) {
-            const T x1 = x[c1], x2 = x[c2];
-            y[c1] = x1;
-            y[c2] = x2;
+            y[c1] = v1;
+            y[c2] = v2;
             continue;
         }
-        const float x1 = ld_f(x + c1), x2 = ld_f(x + c2);
+        const float x1 = ld_f(&v1), x2 = ld_f(&v2);
         st_f(y + c1, x1 * cs.x - x2 * cs.y);
         st_f(y + c2, x2 * cs.x + x1 * cs.y);
     }
