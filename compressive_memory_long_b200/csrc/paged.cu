@@ -279,7 +279,7 @@ template <typename T, int D, int GT>
 int launch_decode(const T *q, const T *k, const T *v, T *kp, T *vp, float *weights, T *out, const PageArgs &a,
                   const DecodeArgs &dc, int64_t most_rows, cudaStream_t st)
 {
-    constexpr size_t smem = kSplitWarps * kStages * (8192 + DecodeTile<T, D>::R * 8) + 3 * GT * D * 4;
+    constexpr size_t smem = kSplitWarps * kStages * (8192 + DecodeTile<T, D>::R * 8) + 2 * GT * D * 4;
     if (!opt_in_smem<k_paged_split<T, D, GT>>(smem)) return INFINI_ERR_CUDA;
     {
         TraceScope trace("paged_split", st);
@@ -292,7 +292,8 @@ int launch_decode(const T *q, const T *k, const T *v, T *kp, T *vp, float *weigh
     int64_t chunks = 1;
     if (weights)   // enough CTAs for every SM several times over; a chunk takes more rows then
         chunks = std::max<int64_t>(1, std::min((most_rows + kJoinRows - 1) / kJoinRows, 2368 / units));
-    return launched(launch_early(k_paged_join<T, D>, dim3((unsigned)units, (unsigned)chunks), kJoinThreads, 0, st, q,
+    return launched(launch_early(k_paged_join<T, D>, dim3((unsigned)units, (unsigned)chunks), kJoinThreads,
+                                 dc.M ? (size_t)4 * dc.hg * D * 4 : 0, st, q,
                                  weights, out, a, dc, k ? 1 : 0));
 }
 

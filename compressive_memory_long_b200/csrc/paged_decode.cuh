@@ -53,43 +53,50 @@ __device__ __forceinline__ int64_t unit_rows(const PageArgs &a, int64_t b, int e
 
 // ---- rotation and small pieces ----------------------------------------------------------------
 
-// Channel c of one rotated head row.
-template <typename T>
-__device__ __forceinline__ float rotated(const T *x, int c, double pos, const DecodeArgs &a)
-{
-    if (!a.freq || c >= a.rot) return ld_f(x + c);
-    const int half = a.rot / 2, i = a.interleaved ? c / 2 : c % half;
-    const bool second = a.interleaved ? (c & 1) : c >= half;
-    const float2 cs = rotary_turn(pos, a.freq[i], a.rot_scale);
-    const float x1 = ld_f(x + (a.interleaved ? 2 * i : i));
-    const float x2 = ld_f(x + (a.interleaved ? 2 * i + 1 : i + half));
-    return second ? x2 * cs.x + x1 * cs.y : x1 * cs.x - x2 * cs.y;
-}
-
-// Rows g0 .. g0 + heads - 1 of q, rotated, into sq [heads][D]; one thread turns a pair of
-// channels of all heads.  Rows up to `fill` are set to 0.
+// Rows 0 .. heads - 1 of q, rotated, into sq [heads][D] (rows up to `fill` are set to 0); with k,
+// one more row, rotated and rounded to the cache's type, into new_k and v into new_v.  A thread
+// turns one pair of channels of every groups-th row; all of its loads are in flight at once.
 template <typename T, int D, int NT>
-__device__ __forceinline__ void load_q(const T *__restrict__ q, int heads, int fill, double pos,
-                                       const DecodeArgs &a, float *sq)
+__device__ __forceinline__ void load_rows(const T *__restrict__ q, int heads, int fill, const T *k, const T *v,
+                                          const int64_t *pos, int64_t row, const DecodeArgs &a, float *sq, T *new_k,
+                                          T *new_v)
 {
-    const int half = a.freq ? a.rot / 2 : 0;
-    for (int i = threadIdx.x; i < D / 2; i += NT) {
-        int c1 = 2 * i, c2 = 2 * i + 1;
-        float2 cs = make_float2(1.f, 0.f);
-        if (i < half) {
-            if (!a.interleaved) {
-                c1 = i;
-                c2 = i + half;
-            }
-            cs = rotary_turn(pos, a.freq[i], a.rot_scale);
-        }
-        for (int g = 0; g < heads; ++g) {
-            const float x1 = ld_f(q + g * D + c1), x2 = ld_f(q + g * D + c2);
-            sq[g * D + c1] = x1 * cs.x - x2 * cs.y;
-            sq[g * D + c2] = x2 * cs.x + x1 * cs.y;
+    constexpr int GROUPS = NT / (D / 2), MOST = (9 + GROUPS - 1) / GROUPS;
+    const int half = a.freq ? a.rot / 2 : 0, i = threadIdx.x % (D / 2), grp = threadIdx.x / (D / 2);
+    const bool turned = i < half, cross = turned && !a.interleaved;
+    const int c1 = cross ? i : 2 * i, c2 = cross ? i + half : 2 * i + 1;
+    float x1[MOST], x2[MOST];
+#pragma unroll
+    for (int e = 0; e < MOST; ++e) {
+        const int g = grp + e * GROUPS;
+        const T *src = g < heads ? q + g * D : k;
+        x1[e] = x2[e] = 0.f;
+        if (g < heads || (g == heads && k)) {
+            x1[e] = ld_f(src + c1);
+            x2[e] = ld_f(src + c2);
         }
     }
-    for (int i = heads * D + threadIdx.x; i < fill * D; i += NT) sq[i] = 0.f;
+    T y = T();
+    if (k && threadIdx.x < D) y = v[threadIdx.x];
+    float2 cs = make_float2(1.f, 0.f);
+    if (turned) cs = rotary_turn((double)(pos ? *pos : row), a.freq[i], a.rot_scale);
+#pragma unroll
+    for (int e = 0; e < MOST; ++e) {
+        const int g = grp + e * GROUPS;
+        // copied channels stay as they are (a product with 0 would spread infinities)
+        const float y1 = turned ? x1[e] * cs.x - x2[e] * cs.y : x1[e];
+        const float y2 = turned ? x2[e] * cs.x + x1[e] * cs.y : x2[e];
+        const bool fresh = g == heads && k;
+        if (fresh) {
+            st_f(new_k + c1, y1);
+            st_f(new_k + c2, y2);
+        }
+        if (g < fill) {                                    // zeros past the heads
+            sq[g * D + c1] = fresh ? 0.f : y1;
+            sq[g * D + c2] = fresh ? 0.f : y2;
+        }
+    }
+    if (k && threadIdx.x < D) new_v[threadIdx.x] = y;
 }
 
 __device__ __forceinline__ uint32_t s_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -155,13 +162,14 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
     constexpr int NO = D / 8;                              // mma: accumulator tiles of 8 channels
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float s_m[kSplitWarps][8], s_l[kSplitWarps][8];
+    __shared__ __align__(16) T s_new[2][D];
     __shared__ ShareScratch s_share;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     unsigned char *stages = smem;                                                // [warp][stage][8 KB]
     float *sq = reinterpret_cast<float *>(smem + kSplitWarps * kStages * 8192);   // [GT][D]
-    float *s_o = sq + GT * D;                                                    // [2][GT][D]
-    int64_t *s_base = reinterpret_cast<int64_t *>(s_o + 2 * GT * D);             // [warp][stage][R]
+    float *s_o = sq;                                                             // [2][GT][D], over sq at a piece's end
+    int64_t *s_base = reinterpret_cast<int64_t *>(sq + 2 * GT * D);             // [warp][stage][R]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int extra = k ? 1 : 0, KH = a.Hkv * dc.HT;
@@ -173,36 +181,44 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
     share_begin<kSplitCtas, NT>(rows_of, dc.B, KH, TR, s_share, t0, t1, rd);
     if (t0 >= t1) return;                // the whole CTA
     Walk ld = rd;
-    int64_t t_ld = t0;
+    int64_t to_load = t1 - t0, left = t1 - t0;
+    int ld_kvh = ld.kh / dc.HT;
+    // a warp's rows of a tile lie in one page, one after the other
+    const bool in_page = (1 << a.shift) >= R;
 
     unsigned char *my = stages + warp * kStages * 8192;
     int64_t *my_base = s_base + warp * kStages * R;
     int pg[RL];
     // page numbers of the next tile to load, one tile ahead of their use
     auto fetch_pages = [&] {
+        const int *table = a.table + (int64_t)ld.b * a.max_pages;
 #pragma unroll
         for (int e = 0; e < RL; ++e) {
             pg[e] = -1;
-            const int64_t r = ld.tile * TR + warp * R + lane + 32 * e;
-            if (t_ld < t1 && lane + 32 * e < R && r < ld.n) {
-                const int64_t i = r >> a.shift;
-                pg[e] = i < a.max_pages ? a.table[ld.b * a.max_pages + i] : -1;
+            const int r = ld.tile * TR + warp * R + lane + 32 * e;
+            if (to_load > 0 && lane + 32 * e < R && r < ld.n) {
+                const int i = r >> a.shift;
+                pg[e] = i < a.max_pages ? table[i] : -1;
             }
         }
     };
+    uint32_t spot[8];            // where this lane's chunks of a stage go
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int ci = i * 32 + lane, r = ci / CPR, c = ci % CPR;
+        spot[i] = (r * CPR + (c ^ Tile::swz(r))) * 16;
+    }
     auto issue = [&](int stage) {
-        if (t_ld < t1) {
-            const int kvh = ld.kh / dc.HT;
-            const int64_t r0 = ld.tile * TR + warp * R, len = ld.n - extra;
+        if (to_load > 0) {
+            const int r0 = ld.tile * TR + warp * R, len = ld.n - extra;
             int64_t base[RL];
 #pragma unroll
             for (int e = 0; e < RL; ++e) {
-                const int64_t r = r0 + lane + 32 * e;
+                const int r = r0 + lane + 32 * e;
                 base[e] = -1;
                 if (lane + 32 * e < R && r < ld.n) {
                     if (pg[e] >= 0 && pg[e] < a.P)
-                        base[e] = ((((int64_t)pg[e] * a.Hkv + kvh) << a.shift) |
-                                   (r & (((int64_t)1 << a.shift) - 1)));
+                        base[e] = ((((int64_t)pg[e] * a.Hkv + ld_kvh) << a.shift) | (r & ((1 << a.shift) - 1)));
                     else
                         g_page_status = 1;
                 }
@@ -210,17 +226,31 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
                 if (r >= len) base[e] = -1;                // the new row comes from k and v
             }
             const uint32_t dk = s_u32(my + stage * 8192);
+            if (in_page) {
+                const int64_t at = __shfl_sync(0xffffffffu, base[0], 0);
+                const int64_t off = (at < 0 ? 0 : at * (CPR * 16)) + lane * 16;
+                const char *ks = reinterpret_cast<const char *>(k_pages) + off;
+                const char *vs = reinterpret_cast<const char *>(v_pages) + off;
+                const int chunks = at < 0 ? 0 : min(len - r0, R) * CPR - lane;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int ci = i * 32 + lane, r = ci / CPR, c = ci % CPR;
-                const int64_t at = __shfl_sync(0xffffffffu, base[RL == 1 ? 0 : (i * 32 / CPR) / 32], r & 31);
-                const int64_t off = (at < 0 ? 0 : at * D) + c * (16 / (int)sizeof(T));
-                const uint32_t dst = dk + (r * CPR + (c ^ Tile::swz(r))) * 16;
-                cp16(dst, k_pages + off, at >= 0);
-                cp16(dst + 4096, v_pages + off, at >= 0);
+                for (int i = 0; i < 8; ++i) {
+                    const bool ok = i * 32 < chunks;
+                    // (a chunk past the rows is not read; its address stays inside the pool)
+                    cp16(dk + spot[i], ok ? ks + i * 512 : reinterpret_cast<const char *>(k_pages), ok);
+                    cp16(dk + spot[i] + 4096, ok ? vs + i * 512 : reinterpret_cast<const char *>(v_pages), ok);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int ci = i * 32 + lane, r = ci / CPR, c = ci % CPR;
+                    const int64_t at = __shfl_sync(0xffffffffu, base[RL == 1 ? 0 : (i * 32 / CPR) / 32], r & 31);
+                    const int64_t off = (at < 0 ? 0 : at * D) + c * (16 / (int)sizeof(T));
+                    cp16(dk + spot[i], k_pages + off, at >= 0);
+                    cp16(dk + spot[i] + 4096, v_pages + off, at >= 0);
+                }
             }
-            walk_next(ld, rows_of, KH, dc.B, TR);
-            ++t_ld;
+            if (walk_next(ld, rows_of, KH, dc.B, TR)) ld_kvh = ld.kh / dc.HT;
+            --to_load;
             fetch_pages();
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -232,17 +262,22 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
     float m[kMma ? 1 : GT], l[kMma ? 1 : GT];
     float o[kMma ? NO : GT][4];
     uint32_t qa[kMma ? D / 16 : 1][4];
+    int stage = 0, kvh = 0, ht = 0, heads = 0, len = 0;
 
-    for (int64_t t = t0; t < t1; ++t) {
-        const int stage = (int)((t - t0) % kStages);
-        issue((int)((t - t0 + kStages - 1) % kStages));
-        const int kvh = rd.kh / dc.HT, ht = rd.kh % dc.HT;
-        const int heads = min(dc.G - ht * dc.hg, dc.hg);
-        const int64_t h0 = rd.b * dc.H + (int64_t)kvh * dc.G + ht * dc.hg;
-        const int64_t len = rd.n - extra;
-        const double pos = !dc.freq ? 0.0 : dc.positions ? (double)dc.positions[rd.b] : (double)len;
-        if (t == t0 || rd.tile == 0) {                     // a piece begins
-            load_q<T, D, NT>(q + h0 * D, heads, GT, pos, dc, sq);
+    for (bool begins = true; left > 0; --left) {
+        issue(stage == 0 ? kStages - 1 : stage - 1);
+        if (begins) {                                      // a piece begins
+            kvh = rd.kh / dc.HT;
+            ht = rd.kh % dc.HT;
+            heads = min(dc.G - ht * dc.hg, dc.hg);
+            len = rd.n - extra;
+            // the new row, if it is in this piece
+            const bool fresh = extra && left >= rd.nt - rd.tile;
+            const int64_t at = ((int64_t)rd.b * a.Hkv + kvh) * D;
+            __syncthreads();                               // the last piece's sums have been read
+            load_rows<T, D, NT>(q + ((int64_t)rd.b * dc.H + (int64_t)kvh * dc.G + ht * dc.hg) * D, heads, GT,
+                                fresh ? k + at : nullptr, v + at, dc.positions ? dc.positions + rd.b : nullptr, len,
+                                dc, sq, s_new[0], s_new[1]);
             __syncthreads();
             if constexpr (kMma) {
                 const float *row = sq + (lane >> 2) * D + (lane & 3) * 2;
@@ -266,52 +301,65 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
         __syncwarp();
         unsigned char *sk = my + stage * 8192, *sv = sk + 4096;
         const int64_t *bs = my_base + stage * R;
-        const int64_t r0 = rd.tile * TR + warp * R;
-        const int mine = (int)min((int64_t)R, rd.n - r0);   // rows of this warp (none: <= 0)
+        const int r0 = rd.tile * TR + warp * R;
+        const int mine = min(R, rd.n - r0);                // rows of this warp (none: <= 0)
         if (extra && r0 <= len && len < r0 + R) {
-            // the new row: rotated, rounded to the cache's type, into the stage and its page
-            const int j = (int)(len - r0);
-            const int64_t src = (rd.b * a.Hkv + kvh) * D, at = bs[j];
-            for (int c = lane; c < D; c += 32) {
-                T x;
-                st_f(&x, rotated(k + src, c, pos, dc));
-                const T y = v[src + c];
-                const int e = 16 / (int)sizeof(T), p = (j * CPR + ((c / e) ^ Tile::swz(j))) * e + c % e;
-                reinterpret_cast<T *>(sk)[p] = x;
-                reinterpret_cast<T *>(sv)[p] = y;
+            // the new row into the stage and its page
+            const int j = len - r0;
+            const int64_t at = bs[j];
+            if (lane < CPR) {
+                const uint4 x = reinterpret_cast<const uint4 *>(s_new[0])[lane];
+                const uint4 y = reinterpret_cast<const uint4 *>(s_new[1])[lane];
+                const int p = j * CPR + (lane ^ Tile::swz(j));
+                reinterpret_cast<uint4 *>(sk)[p] = x;
+                reinterpret_cast<uint4 *>(sv)[p] = y;
                 if (at >= 0 && ht == 0) {
-                    k_pages[at * D + c] = x;
-                    v_pages[at * D + c] = y;
+                    reinterpret_cast<uint4 *>(k_pages)[at * CPR + lane] = x;
+                    reinterpret_cast<uint4 *>(v_pages)[at * CPR + lane] = y;
                 }
             }
             __syncwarp();
         }
-        auto valid = [&](int j) { return j < mine && (bs[j] >= 0 || r0 + j == len); };
+        // the rows to attend to: on a good page, or the new one
+        uint32_t okay[RL];
+#pragma unroll
+        for (int e = 0; e < RL; ++e) {
+            const int j = lane + 32 * e;
+            okay[e] = __ballot_sync(0xffffffffu, j < mine && (bs[j] >= 0 || r0 + j == len));
+        }
         if constexpr (kMma) {
             const uint32_t ka = s_u32(sk), va = s_u32(sv);
             for (int rb = 0; rb < R && rb < mine; rb += 16) {
-                float s[2][4] = {};
+                float s[2][4] = {}, s2[2][4] = {};         // even and odd steps: four chains
                 // keys: matrices (rows 0-7, k 0-7), (rows 0-7, k 8-15), (rows 8-15, ...) x 2
                 const int kr = rb + ((lane >> 4) << 3) + (lane & 7), kc = (lane >> 3) & 1;
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                     uint32_t b[4];
                     ldsm4(ka + (kr * CPR + ((2 * i + kc) ^ Tile::swz(kr))) * 16, b);
-                    mma16816(s[0], qa[i], b[0], b[1]);
-                    mma16816(s[1], qa[i], b[2], b[3]);
+                    mma16816(i & 1 ? s2[0] : s[0], qa[i], b[0], b[1]);
+                    mma16816(i & 1 ? s2[1] : s[1], qa[i], b[2], b[3]);
                 }
+                const uint32_t live = (RL == 1 ? okay[0] : okay[rb >> 5]) >> (rb & 31);
                 float x[2][2], mx = m[0];
 #pragma unroll
                 for (int n8 = 0; n8 < 2; ++n8)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int j = rb + n8 * 8 + (lane & 3) * 2 + e;
-                        const bool ok = valid(j);
-                        x[n8][e] = ok ? (s[n8][e] + s[n8][e + 2]) * sl2 : -INFINITY;
+                        const int j = n8 * 8 + (lane & 3) * 2 + e;
+                        const float y = (s[n8][e] + s2[n8][e]) + (s[n8][e + 2] + s2[n8][e + 2]);
+                        x[n8][e] = live >> j & 1 ? y * sl2 : -INFINITY;
                         mx = fmaxf(mx, x[n8][e]);
-                        if (dc.scores && (lane >> 2) < heads && ok && bs[j] >= 0)
-                            dc.scores[bs[j] * dc.G + ht * dc.hg + (lane >> 2)] = x[n8][e];
                     }
+                if (dc.scores && (lane >> 2) < heads)
+#pragma unroll
+                    for (int n8 = 0; n8 < 2; ++n8)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int j = n8 * 8 + (lane & 3) * 2 + e;
+                            const int64_t at = bs[rb + j];
+                            if ((live >> j & 1) && at >= 0) dc.scores[at * dc.G + ht * dc.hg + (lane >> 2)] = x[n8][e];
+                        }
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 const float at = mx == -INFINITY ? 0.f : mx, corr = exp2f(m[0] - at);
@@ -359,7 +407,7 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
                         s[g] = fmaf(y.x, w.x, fmaf(y.y, w.y, fmaf(y.z, w.z, fmaf(y.w, w.w, s[g]))));
                     }
                 }
-                const bool ok = valid(rb + r);
+                const bool ok = okay[0] >> (rb + r) & 1;          // (R <= 32 here)
                 float p[GT];
 #pragma unroll
                 for (int g = 0; g < GT; ++g) {
@@ -397,7 +445,8 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
             }
         }
         __syncwarp();
-        if (t == t1 - 1 || rd.tile == rd.nt - 1) {         // a piece ends: join the warps
+        begins = rd.tile == rd.nt - 1;
+        if (left == 1 || begins) {                         // a piece ends: join the warps
             if constexpr (kMma) {
                 l[0] += __shfl_xor_sync(0xffffffffu, l[0], 1);
                 l[0] += __shfl_xor_sync(0xffffffffu, l[0], 2);
@@ -460,7 +509,7 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
                 }
                 __syncthreads();
             }
-            const int64_t slot = cta + rd.b * KH + rd.kh;
+            const int64_t slot = cta + (int64_t)rd.b * KH + rd.kh;
             float *po = dc.part_o + slot * dc.hg * D;
             for (int i = tid; i < heads * D; i += NT) po[i] = s_o[i] + s_o[GT * D + i];
             if (tid < heads) {
@@ -473,13 +522,14 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
             }
         }
         walk_next(rd, rows_of, KH, dc.B, TR);
+        stage = stage == kStages - 1 ? 0 : stage + 1;
     }
 }
 
 // ---- the join -----------------------------------------------------------------------------------
 //
 // One CTA per (sequence, key/value head) and chunk of rows.  Chunk 0 reads the memory (before it
-// waits for the split kernel: it depends on the inputs alone), joins the pieces, gates and writes
+// waits for the split kernel: it needs the inputs alone), joins the pieces, gates and writes
 // the output; with weights, every chunk adds its rows' normalised weights from the kept scores.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 1024;      // rows of a chunk
@@ -489,7 +539,8 @@ __global__ void __launch_bounds__(kJoinThreads)
 k_paged_join(const T *__restrict__ q, float *weights, T *__restrict__ out, PageArgs a, DecodeArgs dc, int extra)
 {
     constexpr int TR = DecodeTile<T, D>::TR, NT = kJoinThreads, NW = NT / 32, C4 = D / 4;
-    __shared__ __align__(16) float sq[8 * D], s_num[8 * D];
+    __shared__ __align__(16) float sq[1024];               // 8 rows of q, then the pieces' sums
+    extern __shared__ __align__(16) float s_num[];         // [4][hg * D]
     __shared__ float s_den[8], s_mx[8], s_il[8];
     __shared__ ShareScratch s_share;
     const int64_t b = blockIdx.x / a.Hkv;
@@ -510,18 +561,21 @@ k_paged_join(const T *__restrict__ q, float *weights, T *__restrict__ out, PageA
         return;
     }
     const int64_t unit_b = b * a.Hkv + kvh;
+    if (dc.M && blockIdx.y == 0)                           // on its way while q is rotated
+        for (int i = tid; i < D * D / 32; i += NT)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(dc.M + unit_b * D * D + i * 32));
     int64_t before;
     auto rows_of = [&](int64_t i) { return unit_rows(a, i, extra); };
     const int64_t total = KH * share_count<NT>(rows_of, dc.B, TR, b, s_share, before);
     const int64_t nt = (n + TR - 1) / TR;
-    const double pos = !dc.freq ? 0.0 : dc.positions ? (double)dc.positions[b] : (double)len;
     for (int ht = 0; ht < dc.HT; ++ht) {
         const int heads = min(dc.G - ht * dc.hg, dc.hg);
         if (dc.M && blockIdx.y == 0) {
             // num_g = sigma(q_g) M, den_g = sigma(q_g) . z: a warp takes every NW-th row of M,
             // a lane C4-th of it; the warps' sums meet one after the other
             __syncthreads();
-            load_q<T, D, NT>(q + (h0 + ht * dc.hg) * D, heads, 8, pos, dc, sq);
+            load_rows<T, D, NT>(q + (h0 + ht * dc.hg) * D, heads, 8, nullptr, nullptr,
+                                dc.positions ? dc.positions + b : nullptr, len, dc, sq, nullptr, nullptr);
             __syncthreads();
             for (int i = tid; i < 8 * D; i += NT) sq[i] = i < heads * D ? feature_map(sq[i]) : 0.f;
             __syncthreads();
@@ -531,7 +585,7 @@ k_paged_join(const T *__restrict__ q, float *weights, T *__restrict__ out, PageA
             for (int g = 0; g < 8; ++g) acc[g] = make_float4(0.f, 0.f, 0.f, 0.f);
             const float4 *Mf = reinterpret_cast<const float4 *>(dc.M + unit_b * D * D);
             const int c = lane % C4, sub = lane / C4;
-#pragma unroll 4
+#pragma unroll 8
             for (int f = warp * RW + sub; f < D; f += NW * RW) {
                 const float4 y = __ldcs(Mf + f * C4 + c);
 #pragma unroll
@@ -559,18 +613,21 @@ k_paged_join(const T *__restrict__ q, float *weights, T *__restrict__ out, PageA
                     acc[g].z += __shfl_xor_sync(0xffffffffu, acc[g].z, off);
                     acc[g].w += __shfl_xor_sync(0xffffffffu, acc[g].w, off);
                 }
-            for (int w = 0; w < NW; ++w) {
-                if (warp == w && lane < C4)
+            // warps 4-7, then 0-3 on top of them; the four sums meet at the output
 #pragma unroll
-                    for (int g = 0; g < 8; ++g) {
-                        float4 *y = reinterpret_cast<float4 *>(s_num + g * D) + lane;
-                        float4 x = acc[g];
-                        if (w > 0) {
-                            const float4 z = *y;
-                            x = make_float4(x.x + z.x, x.y + z.y, x.z + z.z, x.w + z.w);
+            for (int turn = 1; turn >= 0; --turn) {
+                if (warp / 4 == turn && lane < C4)
+#pragma unroll
+                    for (int g = 0; g < 8; ++g)
+                        if (g < heads) {
+                            float4 *y = reinterpret_cast<float4 *>(s_num + (warp & 3) * dc.hg * D + g * D) + lane;
+                            float4 x = acc[g];
+                            if (turn == 0) {
+                                const float4 z = *y;
+                                x = make_float4(x.x + z.x, x.y + z.y, x.z + z.z, x.w + z.w);
+                            }
+                            *y = x;
                         }
-                        *y = x;
-                    }
                 __syncthreads();
             }
         }
@@ -604,18 +661,31 @@ k_paged_join(const T *__restrict__ q, float *weights, T *__restrict__ out, PageA
         }
         __syncthreads();
         if (blockIdx.y == 0) {
-            for (int i = tid; i < heads * D; i += NT) {
-                const int g = i / D;
+            // four columns to a thread; the threads left over take every groups-th piece
+            const int cols = heads * C4, groups = NT / cols, col = tid % cols, grp = tid / cols, g = col / C4;
+            if (grp < groups) {
                 const float mx = s_mx[g];
+                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 *po = reinterpret_cast<const float4 *>(dc.part_o) + col;
+#pragma unroll 8
+                for (int64_t c = c0 + grp; c <= c1; c += groups) {
+                    const float4 x = po[(c + unit) * dc.hg * C4];
+                    const float w = mx == -INFINITY ? 0.f : exp2f(dc.part_ml[((c + unit) * dc.hg + g) * 2] - mx);
+                    y = make_float4(fmaf(w, x.x, y.x), fmaf(w, x.y, y.y), fmaf(w, x.z, y.z), fmaf(w, x.w, y.w));
+                }
+                reinterpret_cast<float4 *>(sq)[grp * cols + col] = y;
+            }
+            __syncthreads();
+            for (int i = tid; i < heads * D; i += NT) {
+                const int h = i / D;
                 float y = 0.f;
-#pragma unroll 4
-                for (int64_t c = c0; c <= c1; ++c)
-                    y = fmaf(dc.part_o[(c + unit) * dc.hg * D + i],
-                             mx == -INFINITY ? 0.f : exp2f(dc.part_ml[((c + unit) * dc.hg + g) * 2] - mx), y);
-                y *= s_il[g];
+                for (int k = 0; k < groups; ++k) y += sq[k * cols * 4 + i];
+                y *= s_il[h];
                 if (dc.M) {
-                    const float gt = 1.f / (1.f + expf(-dc.beta[kvh * dc.G + ht * dc.hg + g]));
-                    y = gt * (s_den[g] == 0.f ? 0.f : s_num[i] / s_den[g]) + (1.f - gt) * y;
+                    const float gt = 1.f / (1.f + expf(-dc.beta[kvh * dc.G + ht * dc.hg + h]));
+                    const int w = dc.hg * D;
+                    const float num = (s_num[i] + s_num[w + i]) + (s_num[2 * w + i] + s_num[3 * w + i]);
+                    y = gt * (s_den[h] == 0.f ? 0.f : num / s_den[h]) + (1.f - gt) * y;
                 }
                 st_f(out + (h0 + ht * dc.hg) * D + i, y);
             }

@@ -22,7 +22,9 @@ template <int NC>
 __device__ __forceinline__ int64_t share_from(int64_t c, int64_t total)
 {
     const int64_t C = total < NC ? total : NC;
-    return c >= C ? total : c * total / C;
+    if (c >= C) return total;
+    if (total < (1 << 22)) return (uint32_t)c * (uint32_t)total / (uint32_t)C;   // a shorter division
+    return c * total / C;
 }
 
 // The CTA whose range holds tile t: the largest c with c total / C < t + 1.
@@ -30,6 +32,7 @@ template <int NC>
 __device__ __forceinline__ int64_t share_owner(int64_t t, int64_t total)
 {
     const int64_t C = total < NC ? total : NC;
+    if (total < (1 << 22)) return ((uint32_t)(t + 1) * (uint32_t)C - 1) / (uint32_t)total;
     return ((t + 1) * C - 1) / total;
 }
 
@@ -65,24 +68,26 @@ __device__ __forceinline__ int64_t share_count(const Rows &rows, int64_t B, int 
     return all;
 }
 
-// A tile of the walk through all units.
+// A tile of the walk through all units; walk_next says whether a new unit begins.
 struct Walk {
-    int64_t b, tile, nt, n;      // sequence; tile of the unit, the unit's tiles and rows
-    int kh;                      // head
+    int b, kh;                   // sequence, head
+    int tile, nt;                // tile of the unit, the unit's tiles
+    int n;                       // its rows
 };
 
 template <class Rows>
-__device__ __forceinline__ void walk_next(Walk &w, const Rows &rows, int KH, int64_t B, int TR)
+__device__ __forceinline__ bool walk_next(Walk &w, const Rows &rows, int KH, int64_t B, int TR)
 {
-    if (++w.tile < w.nt) return;
+    if (++w.tile < w.nt) return false;
     w.tile = 0;
-    if (++w.kh < KH) return;
+    if (++w.kh < KH) return true;
     w.kh = 0;
     for (++w.b; w.b < B; ++w.b) {
-        w.n = rows(w.b);
+        w.n = (int)rows(w.b);
         w.nt = (w.n + TR - 1) / TR;
-        if (w.nt > 0) return;
+        if (w.nt > 0) break;
     }
+    return true;
 }
 
 // This CTA's tiles [t0, t1) and where the first one lies.  The whole block calls; with t0 >= t1
@@ -91,16 +96,12 @@ template <int NC, int NT, class Rows>
 __device__ __forceinline__ void share_begin(const Rows &rows, int64_t B, int KH, int TR, ShareScratch &s, int64_t &t0,
                                             int64_t &t1, Walk &w)
 {
-    int64_t none;
-    const int64_t total = KH * share_count<NT>(rows, B, TR, 0, s, none);
-    t0 = t1 = 0;
-    if (total == 0) return;
-    t0 = share_from<NC>(blockIdx.x, total);
-    t1 = share_from<NC>(blockIdx.x + 1, total);
-    if (t0 >= t1) return;
-    const int64_t at = t0 / KH;          // the tile t0 is one of sequence b with before <= at < before + tiles(b)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t base = 0;
+    int64_t total = 0, none;
+    const bool few = B <= NT;            // one look at the lengths serves both passes
+    if (!few) total = KH * share_count<NT>(rows, B, TR, 0, s, none);
+    t0 = t1 = 0;
+    int64_t base = 0, at = 0;
     for (int64_t b0 = 0; b0 < B; b0 += NT) {
         const int64_t b = b0 + threadIdx.x;
         const int64_t mine = b < B ? (rows(b) + TR - 1) / TR : 0;
@@ -113,9 +114,18 @@ __device__ __forceinline__ void share_begin(const Rows &rows, int64_t B, int KH,
         if (lane == 31) s.red[warp] = inc;
         __syncthreads();
         int64_t upto = base + inc, sum = 0;
+#pragma unroll
         for (int i = 0; i < NT / 32; ++i) {
             if (i < warp) upto += s.red[i];
             sum += s.red[i];
+        }
+        if (b0 == 0) {
+            if (few) total = KH * sum;
+            if (total == 0) return;
+            t0 = share_from<NC>(blockIdx.x, total);
+            t1 = share_from<NC>(blockIdx.x + 1, total);
+            if (t0 >= t1) return;
+            at = t0 / KH;    // of the sequence b with before <= at < before + tiles(b)
         }
         if (mine > 0 && upto - mine <= at && at < upto) {
             s.b = b;
@@ -125,12 +135,12 @@ __device__ __forceinline__ void share_begin(const Rows &rows, int64_t B, int KH,
         base += sum;
         if (base > at) break;
     }
-    w.b = s.b;
-    w.n = rows(w.b);
+    w.b = (int)s.b;
+    w.n = (int)rows(w.b);
     w.nt = (w.n + TR - 1) / TR;
     const int64_t in_b = t0 - s.before * KH;
     w.kh = (int)(in_b / w.nt);
-    w.tile = in_b % w.nt;
+    w.tile = (int)(in_b % w.nt);
 }
 
 }  // namespace paged
