@@ -62,14 +62,20 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-__device__ __forceinline__ int peer_ld(const int *p, uint32_t rank)
+__device__ __forceinline__ int2 peer_ld(const int *p, uint32_t rank)
 {
     uint32_t at;
-    int v;
+    int2 v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
                  : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
     return v;
+}
+
+// Sum of the 32 warps' values before this warp's.
+__device__ __forceinline__ int before_warp(const int *per_warp, int warp, int lane)
+{
+    return __reduce_add_sync(0xffffffffu, lane < warp ? per_warp[lane] : 0);
 }
 
 __global__ void __launch_bounds__(kSelectThreads)
@@ -79,7 +85,8 @@ k_evict_select(const float *__restrict__ weights, PageArgs a, EvictArgs e, int C
     extern __shared__ int s_dyn[];
     int *hist = s_dyn;                                               // [3][kBins]
     uint32_t *keys = reinterpret_cast<uint32_t *>(s_dyn + 3 * kBins);   // [cap]
-    __shared__ int s_warp[NW], s_gt[NW], s_eq[NW], s_tot[2];
+    __shared__ int s_warp[NW], s_gt[NW], s_eq[NW];
+    __shared__ __align__(8) int s_tot[2];
     __shared__ int s_digit, s_rank;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t unit = blockIdx.x / CS, b = unit / a.Hkv;
@@ -98,18 +105,18 @@ k_evict_select(const float *__restrict__ weights, PageArgs a, EvictArgs e, int C
     const int per = (old + CS - 1) / CS, r0 = min(rank * per, old), cnt = min(per, old - r0);
     auto load_key = [&](int i) {
         const int64_t row = pool_row(a, table, r0 + i, kvh);
-        return row < 0 ? 0u : weight_key(weights[row]);
+        return row < 0 ? 0u : weight_key(__ldcs(weights + row));
     };
     auto key_of = [&](int i) { return i < cap ? keys[i] : load_key(i); };
     for (int i = tid; i < 3 * kBins; i += NT) hist[i] = 0;
     {
         const int held = min(cnt, cap);
-        for (int i0 = tid; i0 < held; i0 += 4 * NT) {
-            uint32_t x[4];
+        for (int i0 = tid; i0 < held; i0 += 8 * NT) {
+            uint32_t x[8];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) x[u] = i0 + u * NT < held ? load_key(i0 + u * NT) : 0;
+            for (int u = 0; u < 8; ++u) x[u] = i0 + u * NT < held ? load_key(i0 + u * NT) : 0;
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < 8; ++u)
                 if (i0 + u * NT < held) keys[i0 + u * NT] = x[u];
         }
     }
@@ -131,9 +138,17 @@ k_evict_select(const float *__restrict__ weights, PageArgs a, EvictArgs e, int C
             // bins from the top, two per thread: thread tid has bins 2047 - 2 tid and the next
             int x0 = 0, x1 = 0;
             const int top = kBins - 1 - 2 * tid;
-            for (int c = 0; c < CS; ++c) {
-                x0 += CS > 1 ? peer_ld(h + top, c) : h[top];
-                x1 += CS > 1 ? peer_ld(h + top - 1, c) : h[top - 1];
+            if (CS == 1) {
+                x0 = h[top];
+                x1 = h[top - 1];
+            } else {
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    if (c < CS) {
+                        const int2 y = peer_ld(h + top - 1, c);
+                        x0 += y.y;
+                        x1 += y.x;
+                    }
             }
             int inc = x0 + x1;
 #pragma unroll
@@ -143,8 +158,7 @@ k_evict_select(const float *__restrict__ weights, PageArgs a, EvictArgs e, int C
             }
             if (lane == 31) s_warp[warp] = inc;
             __syncthreads();
-            int above = inc - x0 - x1;
-            for (int w = 0; w < warp; ++w) above += s_warp[w];
+            const int above = inc - x0 - x1 + before_warp(s_warp, warp, lane);
             // the digit: the bin where the count from the top reaches `left`
             if (above < left && left <= above + x0 + x1) {
                 const bool first = left <= above + x0;
@@ -170,22 +184,21 @@ k_evict_select(const float *__restrict__ weights, PageArgs a, EvictArgs e, int C
         s_eq[warp] = eq;
     }
     __syncthreads();
-    if (tid < 2) {
-        int sum = 0;
-        for (int w = 0; w < NW; ++w) sum += tid == 0 ? s_gt[w] : s_eq[w];
-        s_tot[tid] = sum;
+    if (warp < 2) {
+        const int sum = __reduce_add_sync(0xffffffffu, warp == 0 ? s_gt[lane] : s_eq[lane]);
+        if (lane == 0) s_tot[warp] = sum;
     }
     if (CS > 1) cluster_sync();
     else __syncthreads();
-    gt = eq = 0;
-    for (int c = 0; c < rank; ++c) {
-        gt += peer_ld(&s_tot[0], c);
-        eq += peer_ld(&s_tot[1], c);
-    }
-    for (int w = 0; w < warp; ++w) {
-        gt += s_gt[w];
-        eq += s_eq[w];
-    }
+    gt = before_warp(s_gt, warp, lane);
+    eq = before_warp(s_eq, warp, lane);
+#pragma unroll
+    for (int c = 0; c < 7; ++c)
+        if (c < rank) {
+            const int2 y = peer_ld(s_tot, c);
+            gt += y.x;
+            eq += y.y;
+        }
     int *gone = e.gone ? e.gone + unit * e.gone_stride : nullptr;
     for (int i = w0; i < w1; i += 32) {
         const uint32_t key = i + lane < w1 ? key_of(i + lane) : 0;
@@ -260,51 +273,61 @@ k_evict_move(T *k_pages, T *v_pages, float *weights, PageArgs a, EvictArgs e, in
 // ---- fold ---------------------------------------------------------------------------------------
 //
 // sum sigma(k) v^T over a head's evicted rows, on tcgen05: A = sigma(K)^T (M = the key features),
-// B = V (N = the value features), both staged row by row (MN-major), 64 rows a step.  M and z are
+// B = V (N = the value features), both staged row by row (MN-major), 64 rows a stage.  M and z are
 // 32-bit sums, so sigma(k) is split into three bf16 parts (24 bits; two would leave 2^-18, more
 // than the sum's own rounding), v into one (bf16, exact) or three (fp32: the six products down to
-// 2^-24 are kept).  The leading product has an accumulator of its own and every step's result is
+// 2^-24 are kept).  The leading product has an accumulator of its own and every 128 rows' result is
 // read out and added in registers: the tensor core's own additions over a long axis lose about
 // one unit per addition, all in one direction.
 //
-// The evicted rows of all heads are shared out evenly over 148 CTAs (share.cuh).  In each, eight
-// loader warps keep a step of rows in flight in registers, form sigma and the parts and sum z;
+// The evicted rows of all heads are shared out evenly over 148 CTAs (share.cuh).  In each, 16
+// loader warps keep a stage of rows in flight in registers, form sigma and the parts and sum z;
 // one thread issues the products; eight warps read the accumulators.  Reading K and V is the
 // bound (4 d bytes a row against 2 d^2 operations); the parts' products are a quarter of the
 // tensor rate at that speed.
 constexpr int kFoldCtas = 148;
-constexpr int kFoldLoaders = 8, kFoldReaders = 8;
-constexpr int kFoldThreads = 32 * (kFoldLoaders + kFoldReaders + 1);
-constexpr int kFoldRows = 64;
+constexpr int kFoldLoaders = 16, kFoldReaders = 8;
+constexpr int kFoldThreads = 32 * (kFoldLoaders + kFoldReaders + 4);
+constexpr int kFoldRows = 128;       // rows of a tile: one reading of the accumulators
+constexpr int kFoldHalf = 64;        // rows of a stage
 
 template <typename T, int D>
 struct FoldTile {
     static constexpr bool kWide = sizeof(T) == 4;
     static constexpr int VP = kWide ? 3 : 1;               // parts of v
-    static constexpr int KB = 2 * kFoldRows * 128;         // bytes of a part: two blocks of 64 columns
+    static constexpr int KB = 2 * kFoldHalf * 128;         // bytes of a part: two blocks of 64 columns
+    static constexpr int LR = kFoldHalf / kFoldLoaders;    // rows of a loader warp
     static constexpr int STAGE = (3 + VP) * KB;
     static constexpr int STAGES = kWide ? 2 : 3;
     static constexpr int SMEM = STAGES * STAGE + 1024;     // rounded up to 1024 inside
     static constexpr int CPR = D * (int)sizeof(T) / 16;    // 16-byte chunks of a row
-    static constexpr int LD = kFoldRows / kFoldLoaders * CPR / 32;   // chunks per lane, tensor and step
+    static constexpr int LD = (LR * CPR + 31) / 32;   // chunks per lane, tensor and step
     static constexpr int E = 16 / (int)sizeof(T);          // channels of a chunk
     static constexpr uint32_t COLS = 4 * D;                // two buffers of two accumulators
 };
 
-__device__ __forceinline__ float sigma_fast(float x)
+// sigma of two values, as max(x, 0) + e^min(x, 0) (a NaN passes through the maximum).
+__device__ __forceinline__ uint64_t sigma2(float x, float y)
 {
-    return x > 0.f ? x + 1.f : tc::ex2(x * 1.4426950408889634f);
+    float p, q;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(p) : "f"(x));
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(q) : "f"(y));
+    const uint64_t e = tc::f2_mul(tc::f2_pack(fminf(x, 0.f), fminf(y, 0.f)),
+                                  tc::f2_pack(1.4426950408889634f, 1.4426950408889634f));
+    float e0, e1;
+    tc::f2_unpack(e, e0, e1);
+    return tc::f2_add(tc::f2_pack(p, q), tc::f2_pack(tc::ex2(e0), tc::ex2(e1)));
 }
 
 // x = h + m + l in bf16 parts, to 2^-25 of it; pairs packed.
-__device__ __forceinline__ void split3(float x, float y, uint32_t (&p)[3])
+__device__ __forceinline__ void split3(uint64_t xy, uint32_t (&p)[3])
 {
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-        p[i] = *reinterpret_cast<const uint32_t *>(&h);
-        x -= __uint_as_float(p[i] << 16);
-        y -= __uint_as_float(p[i] & 0xffff0000u);
+        float x, y;
+        tc::f2_unpack(xy, x, y);
+        p[i] = tc::pack_bf16x2(x, y);
+        if (i < 2) xy = tc::f2_sub(xy, tc::f2_pack(__uint_as_float(p[i] << 16), __uint_as_float(p[i] & 0xffff0000u)));
     }
 }
 
@@ -327,7 +350,7 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
     auto rows_of = [&](int64_t b) { return (int64_t)max(0, cached_rows(a, b) - e.budget); };
     Walk first;
     int64_t t0, t1;
-    share_begin<kFoldCtas, kFoldThreads>(rows_of, e.B, a.Hkv, kFoldRows, s_share, t0, t1, first);
+    share_begin<kFoldCtas, kFoldThreads, 0>(rows_of, e.B, a.Hkv, kFoldRows, s_share, t0, t1, first);
     if (t0 >= t1) return;               // the whole CTA
 
     if (tid == 0) {
@@ -355,21 +378,23 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
     const int64_t steps = t1 - t0;
 
     if (warp < kFoldLoaders) {
-        // a pipeline of its own for each step's addresses: the evicted row's number three steps
-        // ahead, its page two, its data one
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        // Lanes 0-3 look up this warp's rows of a tile's first half, 4-7 those of the second: the
+        // evicted row's number three tiles ahead, its page two, its data one stage.
+        constexpr int LR = Tile::LR;
         Walk ahead = first;
-        int64_t t_ahead = t0;
-        int r1 = -1, kvh1 = 0, r2 = -1, kvh2 = 0, pg2 = -1;
-        int64_t b1 = 0, base3 = -1;
+        int64_t t_ahead = t1 - t0;
+        int r1 = -1, r2 = -1, kvh1 = 0, kvh2 = 0, pg2 = -1, b1 = 0;
+        int64_t base3 = -1;
         auto take_row = [&] {
             r1 = -1;
-            if (t_ahead >= t1) return;
-            const int64_t j = ahead.tile * kFoldRows + warp * 8 + lane;
+            if (t_ahead <= 0) return;
+            const int j = ahead.tile * kFoldRows + lane / LR * kFoldHalf + warp * LR + lane % LR;
             b1 = ahead.b;
             kvh1 = ahead.kh;
-            if (lane < 8 && j < ahead.n) r1 = e.gone[(b1 * a.Hkv + kvh1) * e.gone_stride + j];
-            walk_next(ahead, rows_of, a.Hkv, e.B, kFoldRows);
-            ++t_ahead;
+            if (lane < 2 * LR && j < ahead.n) r1 = e.gone[((int64_t)b1 * a.Hkv + kvh1) * e.gone_stride + j];
+            walk_next<0>(ahead, rows_of, a.Hkv, e.B, kFoldRows);
+            --t_ahead;
         };
         auto take_page = [&] {
             r2 = r1;
@@ -377,7 +402,7 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
             pg2 = -1;
             if (r2 >= 0) {
                 const int i = r2 >> a.shift;
-                pg2 = i < a.max_pages ? a.table[b1 * a.max_pages + i] : -1;
+                pg2 = i < a.max_pages ? a.table[(int64_t)b1 * a.max_pages + i] : -1;
             }
         };
         auto take_base = [&] {
@@ -390,16 +415,18 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
             }
         };
         uint4 rk[LD], rv[LD];
-        bool ok[LD];
-        auto load = [&](int i) {
+        uint32_t ok = 0;                // bit i: chunk i is a row's
+        // chunk i of a stage: row ci / CPR of this warp's, column ci % CPR (the same in every stage)
+        auto load = [&](int i, int h) {
             const int ci = i * 32 + lane;
-            const int64_t at = __shfl_sync(0xffffffffu, base3, ci / CPR);
-            ok[i] = at >= 0;
+            const int64_t at = __shfl_sync(0xffffffffu, base3, h * LR + (ci / CPR) % LR);
+            const bool on = at >= 0 && ci < LR * CPR;
             rk[i] = rv[i] = make_uint4(0, 0, 0, 0);
-            if (at >= 0) {
+            if (on) {
                 rk[i] = __ldcs(reinterpret_cast<const uint4 *>(k_pages) + at * CPR + ci % CPR);
                 rv[i] = __ldcs(reinterpret_cast<const uint4 *>(v_pages) + at * CPR + ci % CPR);
             }
+            ok = on ? ok | 1u << i : ok & ~(1u << i);
         };
         take_row();
         take_page();
@@ -408,84 +435,99 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
         take_page();
         take_row();
 #pragma unroll
-        for (int i = 0; i < LD; ++i) load(i);
-        // chunk ci of every step is the same column of this lane
-        float zs[E];
+        for (int i = 0; i < LD; ++i) load(i, 0);
+        uint64_t zs[E / 2];
 #pragma unroll
-        for (int x = 0; x < E; ++x) zs[x] = 0.f;
+        for (int x = 0; x < E / 2; ++x) zs[x] = 0;
         Walk at = first;
-        for (int64_t t = t0; t < t1; ++t) {
-            const int64_t s = t - t0;
-            const int stage = (int)(s % ST);
-            if (s >= ST && !tc::mbar_wait(&empty[stage], (uint32_t)((s / ST - 1) & 1), abort, 90)) break;
-            take_base();
-            take_page();
-            take_row();
-            unsigned char *sk = base + stage * Tile::STAGE, *sv = sk + 3 * Tile::KB;
+        int stage = 0;
+        uint32_t lap = 0;
+        bool alive = true;
+        for (int64_t left = t1 - t0; left > 0 && alive; --left) {
 #pragma unroll
-            for (int i = 0; i < LD; ++i) {
-                const int ci = i * 32 + lane, r = warp * 8 + ci / CPR, ch = ci % CPR * E;   // row, first channel
-                // column block, then the row's swizzled 16-byte chunk of 8 channels
-                const uint32_t dst = (ch >> 6) * (kFoldRows * 128) + r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4) +
-                                     (ch & 7) * 2;
-                if constexpr (!Tile::kWide) {
-                    const uint32_t w[4] = {rk[i].x, rk[i].y, rk[i].z, rk[i].w};
-                    uint32_t p[4][3];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const float f0 = ok[i] ? sigma_fast(__uint_as_float(w[x] << 16)) : 0.f;
-                        const float f1 = ok[i] ? sigma_fast(__uint_as_float(w[x] & 0xffff0000u)) : 0.f;
-                        zs[2 * x] += f0;
-                        zs[2 * x + 1] += f1;
-                        split3(f0, f1, p[x]);
-                    }
-#pragma unroll
-                    for (int y = 0; y < 3; ++y)
-                        *reinterpret_cast<uint4 *>(sk + y * Tile::KB + dst) = make_uint4(p[0][y], p[1][y], p[2][y], p[3][y]);
-                    *reinterpret_cast<uint4 *>(sv + dst) = rv[i];
-                } else {
-                    const uint32_t w[4] = {rk[i].x, rk[i].y, rk[i].z, rk[i].w};
-                    uint32_t p[2][3], q[2][3];
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const float f0 = ok[i] ? sigma_fast(__uint_as_float(w[2 * x])) : 0.f;
-                        const float f1 = ok[i] ? sigma_fast(__uint_as_float(w[2 * x + 1])) : 0.f;
-                        zs[2 * x] += f0;
-                        zs[2 * x + 1] += f1;
-                        split3(f0, f1, p[x]);
-                    }
-                    split3(__uint_as_float(rv[i].x), __uint_as_float(rv[i].y), q[0]);
-                    split3(__uint_as_float(rv[i].z), __uint_as_float(rv[i].w), q[1]);
-#pragma unroll
-                    for (int y = 0; y < 3; ++y) {
-                        *reinterpret_cast<uint2 *>(sk + y * Tile::KB + dst) = make_uint2(p[0][y], p[1][y]);
-                        *reinterpret_cast<uint2 *>(sv + y * Tile::KB + dst) = make_uint2(q[0][y], q[1][y]);
-                    }
+            for (int h = 0; h < 2; ++h) {
+                if (lap > 0 && alive) alive = tc::mbar_wait(&empty[stage], (lap - 1) & 1, abort, 90);
+                if (h == 1) {           // what is loaded from here on is the next tile's first half
+                    take_base();
+                    take_page();
+                    take_row();
                 }
-                load(i);                // the next step's chunk into the registers just read
-            }
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&full[stage]);
-            if (t == t1 - 1 || at.tile == at.nt - 1) {   // a piece ends: this warp's part of z
-                const int64_t slot = blockIdx.x + at.b * a.Hkv + at.kh;
+                unsigned char *sk = base + stage * Tile::STAGE, *sv = sk + 3 * Tile::KB;
 #pragma unroll
-                for (int x = 0; x < E; ++x) {
+                for (int i = 0; i < LD; ++i) {
+                    const int ci = i * 32 + lane, r = warp * LR + ci / CPR, ch = ci % CPR * E;   // row, first channel
+                    // column block, then the row's swizzled 16-byte chunk of 8 channels
+                    const uint32_t dst = (ch >> 6) * (kFoldHalf * 128) + r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4) +
+                                         (ch & 7) * 2;
+                    const bool on = ok >> i & 1, mine = ci < LR * CPR;
+                    const uint32_t w[4] = {rk[i].x, rk[i].y, rk[i].z, rk[i].w};
+                    uint32_t p[E / 2][3];
 #pragma unroll
-                    for (int off = CPR; off < 32; off <<= 1) zs[x] += __shfl_xor_sync(0xffffffffu, zs[x], off);
-                    if (lane < CPR) e.part_z[(slot * kFoldLoaders + warp) * D + lane * E + x] = zs[x];
-                    zs[x] = 0.f;
+                    for (int x = 0; x < E / 2; ++x) {
+                        uint64_t f;
+                        if constexpr (Tile::kWide) f = sigma2(__uint_as_float(w[2 * x]), __uint_as_float(w[2 * x + 1]));
+                        else f = sigma2(__uint_as_float(w[x] << 16), __uint_as_float(w[x] & 0xffff0000u));
+                        f = on ? f : 0;
+                        zs[x] = tc::f2_add(zs[x], f);
+                        split3(f, p[x]);
+                    }
+                    if (mine) {
+                        if constexpr (!Tile::kWide) {
+#pragma unroll
+                            for (int y = 0; y < 3; ++y)
+                                *reinterpret_cast<uint4 *>(sk + y * Tile::KB + dst) =
+                                    make_uint4(p[0][y], p[1][y], p[2][y], p[3][y]);
+                            *reinterpret_cast<uint4 *>(sv + dst) = rv[i];
+                        } else {
+                            uint32_t q[2][3];
+                            split3(tc::f2_pack(__uint_as_float(rv[i].x), __uint_as_float(rv[i].y)), q[0]);
+                            split3(tc::f2_pack(__uint_as_float(rv[i].z), __uint_as_float(rv[i].w)), q[1]);
+#pragma unroll
+                            for (int y = 0; y < 3; ++y) {
+                                *reinterpret_cast<uint2 *>(sk + y * Tile::KB + dst) = make_uint2(p[0][y], p[1][y]);
+                                *reinterpret_cast<uint2 *>(sv + y * Tile::KB + dst) = make_uint2(q[0][y], q[1][y]);
+                            }
+                        }
+                    }
+                    load(i, h ^ 1);     // the next stage's chunk into the registers just read
+                }
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&full[stage]);
+                if (++stage == ST) {
+                    stage = 0;
+                    ++lap;
                 }
             }
-            walk_next(at, rows_of, a.Hkv, e.B, kFoldRows);
+            if (left == 1 || at.tile == at.nt - 1) {   // a piece ends: this warp's part of z
+                const int64_t slot = blockIdx.x + (int64_t)at.b * a.Hkv + at.kh;
+#pragma unroll
+                for (int x = 0; x < E / 2; ++x) {
+                    float z0, z1;
+                    tc::f2_unpack(zs[x], z0, z1);
+#pragma unroll
+                    for (int off = CPR; off < 32; off <<= 1) {
+                        z0 += __shfl_xor_sync(0xffffffffu, z0, off);
+                        z1 += __shfl_xor_sync(0xffffffffu, z1, off);
+                    }
+                    if (lane < CPR) {
+                        float *z = e.part_z + (slot * kFoldLoaders + warp) * D + lane * E + 2 * x;
+                        z[0] = z0;
+                        z[1] = z1;
+                    }
+                    zs[x] = 0;
+                }
+            }
+            walk_next<0>(at, rows_of, a.Hkv, e.B, kFoldRows);
         }
     } else if (warp < kFoldLoaders + kFoldReaders) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         // reader w: lanes 32 (w % 4) .. + 31 (key features), half w / 4 of the columns
         const int w = warp - kFoldLoaders, part = warp & 3, half = w >> 2, f = part * 32 + lane;
         constexpr int NC = D / 2;       // columns of a half
-        float acc[NC];
+        uint64_t acc[NC / 2];           // pairs of columns
 #pragma unroll
-        for (int i = 0; i < NC; ++i) acc[i] = 0.f;
+        for (int i = 0; i < NC / 2; ++i) acc[i] = 0;
         Walk at = first;
         for (int64_t t = t0; t < t1; ++t) {
             const int64_t s = t - t0;
@@ -501,7 +543,11 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
                     tc::tmem_ld16(col + D + c, y);
                     tc::tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[c + i] += __uint_as_float(x[i]) + __uint_as_float(y[i]);
+                    for (int i = 0; i < 16; i += 2)
+                        acc[(c + i) / 2] = tc::f2_add(
+                            acc[(c + i) / 2],
+                            tc::f2_add(tc::f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
+                                       tc::f2_pack(__uint_as_float(y[i]), __uint_as_float(y[i + 1]))));
                 }
             }
             tc::tc_fence_before();
@@ -509,7 +555,7 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
             if (lane == 0) tc::mbar_arrive(&tempty[buf]);
             if (t == t1 - 1 || at.tile == at.nt - 1) {
                 if (part * 32 < D) {
-                    const int64_t unit = at.b * a.Hkv + at.kh;
+                    const int64_t unit = (int64_t)at.b * a.Hkv + at.kh;
                     // a head that is this CTA's alone goes into its memory at once
                     const bool whole = t - t0 >= at.nt - 1 && at.tile == at.nt - 1;
                     float4 *dst = whole ? reinterpret_cast<float4 *>(M + unit * D * D + f * D + half * NC)
@@ -517,7 +563,9 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
                                                                      half * NC * D + f * 4);
 #pragma unroll
                     for (int c = 0; c < NC; c += 4) {
-                        float4 x = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+                        float4 x;
+                        tc::f2_unpack(acc[c / 2], x.x, x.y);
+                        tc::f2_unpack(acc[c / 2 + 1], x.z, x.w);
                         float4 *p = dst + (whole ? c / 4 : c / 4 * D);   // pieces: [c / 4][f][4]
                         if (whole) {
                             const float4 y = *p;
@@ -527,42 +575,53 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < NC; ++i) acc[i] = 0.f;
+                for (int i = 0; i < NC / 2; ++i) acc[i] = 0;
             }
-            walk_next(at, rows_of, a.Hkv, e.B, kFoldRows);
+            walk_next<0>(at, rows_of, a.Hkv, e.B, kFoldRows);
         }
-    } else if (lane == 0) {
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 24;");
+      if (warp == kFoldLoaders + kFoldReaders && lane == 0) {
         constexpr uint32_t idesc = tc::idesc_bf16(128, D, 1, 1);
+        int stage = 0;
+        uint32_t lap = 0;
         for (int64_t s = 0; s < steps; ++s) {
-            const int stage = (int)(s % ST), buf = (int)(s & 1);
+            const int buf = (int)(s & 1);
             if (s >= 2 && !tc::mbar_wait(&tempty[buf], (uint32_t)(((s >> 1) - 1) & 1), abort, 92)) break;
-            if (!tc::mbar_wait(&full[stage], (uint32_t)((s / ST) & 1), abort, 93)) break;
-            tc::tc_fence_after();
-            const uint32_t sk = tc::smem_u32(base + stage * Tile::STAGE), sv = sk + 3 * Tile::KB;
             const uint32_t d0 = tmem + buf * 2 * D, d1 = d0 + D;
-            uint32_t on = 0;
+            for (int h = 0; h < 2; ++h) {
+                if (!tc::mbar_wait(&full[stage], lap & 1, abort, 93)) break;
+                tc::tc_fence_after();
+                const uint32_t sk = tc::smem_u32(base + stage * Tile::STAGE), sv = sk + 3 * Tile::KB;
+                uint32_t on = h;
 #pragma unroll
-            for (int i = 0; i < 3; ++i)
+                for (int i = 0; i < 3; ++i)
 #pragma unroll
-                for (int j = 0; j < VP; ++j) {
-                    if (i + j > 2) continue;
-                    for (int kk = 0; kk < kFoldRows / 16; ++kk) {
-                        const uint64_t da = tc::sdesc_sw128(sk + i * Tile::KB + kk * 2048, kFoldRows * 128, 1024);
-                        const uint64_t db = tc::sdesc_sw128(sv + j * Tile::KB + kk * 2048, kFoldRows * 128, 1024);
-                        if (i + j == 0) {
-                            tc::mma_ss(d0, da, db, idesc, kk > 0);
-                        } else {
-                            tc::mma_ss(d1, da, db, idesc, on);
-                            on = 1;
+                    for (int j = 0; j < VP; ++j) {
+                        if (i + j > 2) continue;
+                        for (int kk = 0; kk < kFoldHalf / 16; ++kk) {
+                            const uint64_t da = tc::sdesc_sw128(sk + i * Tile::KB + kk * 2048, kFoldHalf * 128, 1024);
+                            const uint64_t db = tc::sdesc_sw128(sv + j * Tile::KB + kk * 2048, kFoldHalf * 128, 1024);
+                            if (i + j == 0) {
+                                tc::mma_ss(d0, da, db, idesc, h + kk > 0);
+                            } else {
+                                tc::mma_ss(d1, da, db, idesc, on);
+                                on = 1;
+                            }
                         }
                     }
+                tc::mma_commit(&empty[stage]);
+                if (++stage == ST) {
+                    stage = 0;
+                    ++lap;
                 }
-            tc::mma_commit(&empty[stage]);
+            }
             tc::mma_commit(&tfull[buf]);
         }
         // the last products end before TMEM is given back
         for (int64_t s = steps > 2 ? steps - 2 : 0; s < steps; ++s)
             tc::mbar_wait(&tfull[s & 1], (uint32_t)((s >> 1) & 1), abort, 94);
+      }
     }
     __syncwarp();
     tc::tc_fence_before();
@@ -585,7 +644,7 @@ k_evict_reduce(PageArgs a, EvictArgs e, float *M, float *z)
     const int64_t n = rows_of(b), nt = (n + kFoldRows - 1) / kFoldRows;
     if (n == 0) return;
     int64_t before;
-    const int64_t total = a.Hkv * share_count<256>(rows_of, e.B, kFoldRows, b, s_share, before);
+    const int64_t total = a.Hkv * share_count<256, 0>(rows_of, e.B, kFoldRows, b, s_share, before);
     const int64_t s = before * a.Hkv + kvh * nt;
     const int64_t c0 = share_owner<kFoldCtas>(s, total), c1 = share_owner<kFoldCtas>(s + nt - 1, total);
     if (c0 != c1) {

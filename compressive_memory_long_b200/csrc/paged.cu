@@ -290,8 +290,8 @@ int launch_decode(const T *q, const T *k, const T *v, T *kp, T *vp, float *weigh
     TraceScope trace("paged_join", st);
     const int64_t units = dc.B * a.Hkv;
     int64_t chunks = 1;
-    if (weights)   // enough CTAs for every SM several times over; a chunk takes more rows then
-        chunks = std::max<int64_t>(1, std::min((most_rows + kJoinRows - 1) / kJoinRows, 2368 / units));
+    if (weights)   // no more CTAs than are resident at once (they all wait); a chunk loops over its rows
+        chunks = std::max<int64_t>(1, std::min((most_rows + kJoinRows - 1) / kJoinRows, kSplitCtas / units));
     return launched(launch_early(k_paged_join<T, D>, dim3((unsigned)units, (unsigned)chunks), kJoinThreads,
                                  dc.M ? (size_t)4 * dc.hg * D * 4 : 0, st, q,
                                  weights, out, a, dc, k ? 1 : 0));

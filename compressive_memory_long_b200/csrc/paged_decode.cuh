@@ -55,49 +55,67 @@ __device__ __forceinline__ int64_t unit_rows(const PageArgs &a, int64_t b, int e
 
 // Rows 0 .. heads - 1 of q, rotated, into sq [heads][D] (rows up to `fill` are set to 0); with k,
 // one more row, rotated and rounded to the cache's type, into new_k and v into new_v.  A thread
-// turns one pair of channels of every groups-th row; all of its loads are in flight at once.
+// turns one pair of channels of every GROUPS-th row.  Two halves: `load` puts all loads in flight,
+// `store` uses them, so that other loads can be issued between.
 template <typename T, int D, int NT>
-__device__ __forceinline__ void load_rows(const T *__restrict__ q, int heads, int fill, const T *k, const T *v,
-                                          const int64_t *pos, int64_t row, const DecodeArgs &a, float *sq, T *new_k,
-                                          T *new_v)
-{
-    constexpr int GROUPS = NT / (D / 2), MOST = (9 + GROUPS - 1) / GROUPS;
-    const int half = a.freq ? a.rot / 2 : 0, i = threadIdx.x % (D / 2), grp = threadIdx.x / (D / 2);
-    const bool turned = i < half, cross = turned && !a.interleaved;
-    const int c1 = cross ? i : 2 * i, c2 = cross ? i + half : 2 * i + 1;
+struct RowLoad {
+    static constexpr int GROUPS = NT / (D / 2), MOST = (9 + GROUPS - 1) / GROUPS;
     float x1[MOST], x2[MOST];
+    double freq;
+    int64_t pos;
+    T y;
+    int heads, c1, c2;
+    bool fresh, turned;
+
+    __device__ __forceinline__ void load(const T *__restrict__ q, int heads_, const T *k, const T *v, const int64_t *at,
+                                         int64_t row, const DecodeArgs &a)
+    {
+        const int half = a.freq ? a.rot / 2 : 0, i = threadIdx.x % (D / 2), grp = threadIdx.x / (D / 2);
+        heads = heads_;
+        fresh = k != nullptr;
+        turned = i < half;
+        const bool cross = turned && !a.interleaved;
+        c1 = cross ? i : 2 * i;
+        c2 = cross ? i + half : 2 * i + 1;
+        pos = at ? *at : row;
+        freq = turned ? a.freq[i] : 0.0;
 #pragma unroll
-    for (int e = 0; e < MOST; ++e) {
-        const int g = grp + e * GROUPS;
-        const T *src = g < heads ? q + g * D : k;
-        x1[e] = x2[e] = 0.f;
-        if (g < heads || (g == heads && k)) {
-            x1[e] = ld_f(src + c1);
-            x2[e] = ld_f(src + c2);
+        for (int e = 0; e < MOST; ++e) {
+            const int g = grp + e * GROUPS;
+            const T *src = g < heads ? q + g * D : k;
+            x1[e] = x2[e] = 0.f;
+            if (g < heads || (g == heads && fresh)) {
+                x1[e] = ld_f(src + c1);
+                x2[e] = ld_f(src + c2);
+            }
         }
+        if (fresh && threadIdx.x < D) y = v[threadIdx.x];
     }
-    T y = T();
-    if (k && threadIdx.x < D) y = v[threadIdx.x];
-    float2 cs = make_float2(1.f, 0.f);
-    if (turned) cs = rotary_turn((double)(pos ? *pos : row), a.freq[i], a.rot_scale);
+
+    __device__ __forceinline__ void store(int fill, const DecodeArgs &a, float *sq, T *new_k, T *new_v) const
+    {
+        const int grp = threadIdx.x / (D / 2);
+        float2 cs = make_float2(1.f, 0.f);
+        if (turned) cs = rotary_turn((double)pos, freq, a.rot_scale);
 #pragma unroll
-    for (int e = 0; e < MOST; ++e) {
-        const int g = grp + e * GROUPS;
-        // copied channels stay as they are (a product with 0 would spread infinities)
-        const float y1 = turned ? x1[e] * cs.x - x2[e] * cs.y : x1[e];
-        const float y2 = turned ? x2[e] * cs.x + x1[e] * cs.y : x2[e];
-        const bool fresh = g == heads && k;
-        if (fresh) {
-            st_f(new_k + c1, y1);
-            st_f(new_k + c2, y2);
+        for (int e = 0; e < MOST; ++e) {
+            const int g = grp + e * GROUPS;
+            // copied channels stay as they are (a product with 0 would spread infinities)
+            const float y1 = turned ? x1[e] * cs.x - x2[e] * cs.y : x1[e];
+            const float y2 = turned ? x2[e] * cs.x + x1[e] * cs.y : x2[e];
+            const bool last = g == heads && fresh;
+            if (last) {
+                st_f(new_k + c1, y1);
+                st_f(new_k + c2, y2);
+            }
+            if (g < fill) {                                // zeros past the heads
+                sq[g * D + c1] = last ? 0.f : y1;
+                sq[g * D + c2] = last ? 0.f : y2;
+            }
         }
-        if (g < fill) {                                    // zeros past the heads
-            sq[g * D + c1] = fresh ? 0.f : y1;
-            sq[g * D + c2] = fresh ? 0.f : y2;
-        }
+        if (fresh && threadIdx.x < D) new_v[threadIdx.x] = y;
     }
-    if (k && threadIdx.x < D) new_v[threadIdx.x] = y;
-}
+};
 
 __device__ __forceinline__ uint32_t s_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -178,10 +196,26 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
     int64_t t0, t1;
     Walk rd;
     auto rows_of = [&](int64_t b) { return unit_rows(a, b, extra); };
-    share_begin<kSplitCtas, NT>(rows_of, dc.B, KH, TR, s_share, t0, t1, rd);
+    share_begin<kSplitCtas, NT, 1>(rows_of, dc.B, KH, TR, s_share, t0, t1, rd);
     if (t0 >= t1) return;                // the whole CTA
+    // tile 0 of a unit has no rows: skipped wherever it is met (`left` counts it all the same)
+    int64_t left = t1 - t0;
+    if (rd.tile == 0) {
+        rd.tile = 1;
+        --left;
+    }
+    if (left == 0) return;
+    auto next = [&](Walk &w, int64_t &count) {
+        const bool fresh = walk_next<1>(w, rows_of, KH, dc.B, TR);
+        --count;
+        if (fresh && count > 0) {
+            w.tile = 1;
+            --count;
+        }
+        return fresh;
+    };
     Walk ld = rd;
-    int64_t to_load = t1 - t0, left = t1 - t0;
+    int64_t to_load = left;
     int ld_kvh = ld.kh / dc.HT;
     // a warp's rows of a tile lie in one page, one after the other
     const bool in_page = (1 << a.shift) >= R;
@@ -189,14 +223,14 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
     unsigned char *my = stages + warp * kStages * 8192;
     int64_t *my_base = s_base + warp * kStages * R;
     int pg[RL];
-    // page numbers of the next tile to load, one tile ahead of their use
-    auto fetch_pages = [&] {
-        const int *table = a.table + (int64_t)ld.b * a.max_pages;
+    // page numbers of a tile to load, one tile ahead of their use
+    auto fetch_pages = [&](const Walk &w, int64_t count, int (&pg)[RL]) {
+        const int *table = a.table + (int64_t)w.b * a.max_pages;
 #pragma unroll
         for (int e = 0; e < RL; ++e) {
             pg[e] = -1;
-            const int r = ld.tile * TR + warp * R + lane + 32 * e;
-            if (to_load > 0 && lane + 32 * e < R && r < ld.n) {
+            const int r = (w.tile - 1) * TR + warp * R + lane + 32 * e;
+            if (count > 0 && lane + 32 * e < R && r < w.n) {
                 const int i = r >> a.shift;
                 pg[e] = i < a.max_pages ? table[i] : -1;
             }
@@ -208,9 +242,9 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
         const int ci = i * 32 + lane, r = ci / CPR, c = ci % CPR;
         spot[i] = (r * CPR + (c ^ Tile::swz(r))) * 16;
     }
-    auto issue = [&](int stage) {
+    auto issue = [&](int stage, const int (&pg)[RL]) {
         if (to_load > 0) {
-            const int r0 = ld.tile * TR + warp * R, len = ld.n - extra;
+            const int r0 = (ld.tile - 1) * TR + warp * R, len = ld.n - extra;
             int64_t base[RL];
 #pragma unroll
             for (int e = 0; e < RL; ++e) {
@@ -249,35 +283,50 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
                     cp16(dk + spot[i] + 4096, v_pages + off, at >= 0);
                 }
             }
-            if (walk_next(ld, rows_of, KH, dc.B, TR)) ld_kvh = ld.kh / dc.HT;
-            --to_load;
-            fetch_pages();
+            if (next(ld, to_load)) ld_kvh = ld.kh / dc.HT;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    fetch_pages();
-    for (int s = 0; s < kStages - 1; ++s) issue(s);
+    int kvh = 0, ht = 0, heads = 0, len = 0;
+    RowLoad<T, D, NT> rows;
+    auto begin_piece = [&] {
+        kvh = rd.kh / dc.HT;
+        ht = rd.kh % dc.HT;
+        heads = min(dc.G - ht * dc.hg, dc.hg);
+        len = rd.n - extra;
+        const bool fresh = extra && left >= rd.nt - rd.tile;   // the new row is in this piece
+        const int64_t at = ((int64_t)rd.b * a.Hkv + kvh) * D;
+        rows.load(q + ((int64_t)rd.b * dc.H + (int64_t)kvh * dc.G + ht * dc.hg) * D, heads, fresh ? k + at : nullptr,
+                  v + at, dc.positions ? dc.positions + rd.b : nullptr, len, dc);
+    };
+    {   // the first two tiles' pages and the first piece's rows travel together
+        static_assert(kStages == 3, "two tiles are issued ahead");
+        int pg2[RL];
+        Walk w = ld;
+        int64_t count = to_load;
+        fetch_pages(w, count, pg);
+        next(w, count);
+        fetch_pages(w, count, pg2);
+        begin_piece();
+        issue(0, pg);
+        issue(1, pg2);
+        fetch_pages(ld, to_load, pg);
+    }
 
     const float sl2 = rsqrtf((float)D) * 1.4426950408889634f;
     float m[kMma ? 1 : GT], l[kMma ? 1 : GT];
     float o[kMma ? NO : GT][4];
     uint32_t qa[kMma ? D / 16 : 1][4];
-    int stage = 0, kvh = 0, ht = 0, heads = 0, len = 0;
+    int stage = 0;
 
-    for (bool begins = true; left > 0; --left) {
-        issue(stage == 0 ? kStages - 1 : stage - 1);
+    for (bool begins = true, first = true; left > 0;) {
+        issue(stage == 0 ? kStages - 1 : stage - 1, pg);
+        fetch_pages(ld, to_load, pg);
         if (begins) {                                      // a piece begins
-            kvh = rd.kh / dc.HT;
-            ht = rd.kh % dc.HT;
-            heads = min(dc.G - ht * dc.hg, dc.hg);
-            len = rd.n - extra;
-            // the new row, if it is in this piece
-            const bool fresh = extra && left >= rd.nt - rd.tile;
-            const int64_t at = ((int64_t)rd.b * a.Hkv + kvh) * D;
+            if (!first) begin_piece();
+            first = false;
             __syncthreads();                               // the last piece's sums have been read
-            load_rows<T, D, NT>(q + ((int64_t)rd.b * dc.H + (int64_t)kvh * dc.G + ht * dc.hg) * D, heads, GT,
-                                fresh ? k + at : nullptr, v + at, dc.positions ? dc.positions + rd.b : nullptr, len,
-                                dc, sq, s_new[0], s_new[1]);
+            rows.store(GT, dc, sq, s_new[0], s_new[1]);
             __syncthreads();
             if constexpr (kMma) {
                 const float *row = sq + (lane >> 2) * D + (lane & 3) * 2;
@@ -301,7 +350,7 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
         __syncwarp();
         unsigned char *sk = my + stage * 8192, *sv = sk + 4096;
         const int64_t *bs = my_base + stage * R;
-        const int r0 = rd.tile * TR + warp * R;
+        const int r0 = (rd.tile - 1) * TR + warp * R;
         const int mine = min(R, rd.n - r0);                // rows of this warp (none: <= 0)
         if (extra && r0 <= len && len < r0 + R) {
             // the new row into the stage and its page
@@ -521,16 +570,17 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
                 dc.part_ml[(slot * dc.hg + tid) * 2 + 1] = ls;
             }
         }
-        walk_next(rd, rows_of, KH, dc.B, TR);
+        next(rd, left);
         stage = stage == kStages - 1 ? 0 : stage + 1;
     }
 }
 
 // ---- the join -----------------------------------------------------------------------------------
 //
-// One CTA per (sequence, key/value head) and chunk of rows.  Chunk 0 reads the memory (before it
-// waits for the split kernel: it needs the inputs alone), joins the pieces, gates and writes
-// the output; with weights, every chunk adds its rows' normalised weights from the kept scores.
+// One CTA per (sequence, key/value head) and chunk of rows.  What needs the inputs alone comes
+// before the wait for the split kernel: the memory's part of chunk 0, and with weights the rows'
+// places and what they have so far.  Then chunk 0 joins the pieces, gates and writes the output,
+// and every chunk adds its rows' normalised weights from the kept scores.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 1024;      // rows of a chunk
 
@@ -538,7 +588,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads)
 k_paged_join(const T *__restrict__ q, float *weights, T *__restrict__ out, PageArgs a, DecodeArgs dc, int extra)
 {
-    constexpr int TR = DecodeTile<T, D>::TR, NT = kJoinThreads, NW = NT / 32, C4 = D / 4;
+    constexpr int TR = DecodeTile<T, D>::TR, NT = kJoinThreads, NW = NT / 32, C4 = D / 4, PER = kJoinRows / NT;
     __shared__ __align__(16) float sq[1024];               // 8 rows of q, then the pieces' sums
     extern __shared__ __align__(16) float s_num[];         // [4][hg * D]
     __shared__ float s_den[8], s_mx[8], s_il[8];
@@ -561,21 +611,46 @@ k_paged_join(const T *__restrict__ q, float *weights, T *__restrict__ out, PageA
         return;
     }
     const int64_t unit_b = b * a.Hkv + kvh;
-    if (dc.M && blockIdx.y == 0)                           // on its way while q is rotated
-        for (int i = tid; i < D * D / 32; i += NT)
+    const bool mem = dc.M && blockIdx.y == 0;
+    RowLoad<T, D, NT> rows;
+    auto load_q = [&](int ht, int heads) {
+        rows.load(q + (h0 + ht * dc.hg) * D, heads, nullptr, nullptr, dc.positions ? dc.positions + b : nullptr, len, dc);
+    };
+    if (mem) {
+        for (int i = tid; i < D * D / 32; i += NT)         // on its way while q is rotated
             asm volatile("prefetch.global.L2 [%0];" ::"l"(dc.M + unit_b * D * D + i * 32));
+        load_q(0, min(dc.G, dc.hg));
+    }
+    // a thread's rows of a chunk: their places and weights
+    int64_t place[PER];
+    float so_far[PER];
+    auto load_weights = [&](int64_t j0) {
+        const int *table = a.table + b * a.max_pages;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            const int64_t j = j0 + e * NT + tid;
+            place[e] = j < n ? pool_row(a, table, j, kvh) : -1;
+        }
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            const int64_t j = j0 + e * NT + tid;
+            so_far[e] = place[e] >= 0 && j != len ? weights[place[e]] : 0.f;   // the new row starts at 0
+        }
+    };
+    if (weights) load_weights((int64_t)blockIdx.y * kJoinRows);
     int64_t before;
     auto rows_of = [&](int64_t i) { return unit_rows(a, i, extra); };
-    const int64_t total = KH * share_count<NT>(rows_of, dc.B, TR, b, s_share, before);
-    const int64_t nt = (n + TR - 1) / TR;
+    const int64_t total = KH * share_count<NT, 1>(rows_of, dc.B, TR, b, s_share, before);
+    const int64_t nt = share_tiles<1>(n, TR);
     for (int ht = 0; ht < dc.HT; ++ht) {
         const int heads = min(dc.G - ht * dc.hg, dc.hg);
-        if (dc.M && blockIdx.y == 0) {
+        const float beta = mem && tid < heads ? dc.beta[kvh * dc.G + ht * dc.hg + tid] : 0.f;
+        if (mem) {
             // num_g = sigma(q_g) M, den_g = sigma(q_g) . z: a warp takes every NW-th row of M,
-            // a lane C4-th of it; the warps' sums meet one after the other
+            // a lane four columns
+            if (ht > 0) load_q(ht, heads);
             __syncthreads();
-            load_rows<T, D, NT>(q + (h0 + ht * dc.hg) * D, heads, 8, nullptr, nullptr,
-                                dc.positions ? dc.positions + b : nullptr, len, dc, sq, nullptr, nullptr);
+            rows.store(8, dc, sq, nullptr, nullptr);
             __syncthreads();
             for (int i = tid; i < 8 * D; i += NT) sq[i] = i < heads * D ? feature_map(sq[i]) : 0.f;
             __syncthreads();
@@ -589,16 +664,18 @@ k_paged_join(const T *__restrict__ q, float *weights, T *__restrict__ out, PageA
             for (int f = warp * RW + sub; f < D; f += NW * RW) {
                 const float4 y = __ldcs(Mf + f * C4 + c);
 #pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    const float w = sq[g * D + f];
-                    acc[g].x = fmaf(w, y.x, acc[g].x);
-                    acc[g].y = fmaf(w, y.y, acc[g].y);
-                    acc[g].z = fmaf(w, y.z, acc[g].z);
-                    acc[g].w = fmaf(w, y.w, acc[g].w);
-                }
+                for (int g = 0; g < 8; ++g)
+                    if (g < heads) {
+                        const float w = sq[g * D + f];
+                        acc[g].x = fmaf(w, y.x, acc[g].x);
+                        acc[g].y = fmaf(w, y.y, acc[g].y);
+                        acc[g].z = fmaf(w, y.z, acc[g].z);
+                        acc[g].w = fmaf(w, y.w, acc[g].w);
+                    }
             }
             if (warp < heads) {
                 float part = 0.f;
+#pragma unroll
                 for (int f = lane; f < D; f += 32) part = fmaf(sq[warp * D + f], dc.z[unit_b * D + f], part);
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
@@ -632,28 +709,32 @@ k_paged_join(const T *__restrict__ q, float *weights, T *__restrict__ out, PageA
             }
         }
         if (ht == 0) wait_split();
-        // the unit's pieces: CTAs c0 .. c1 of the split kernel
+        // the unit's pieces: CTAs c0 .. c1 of the split kernel (its first tile has no rows)
         const int64_t unit = b * KH + kvh * dc.HT + ht;
         int64_t c0 = 0, c1 = -1;
         if (n > 0) {
             const int64_t s = before * KH + (kvh * dc.HT + ht) * nt;
-            c0 = share_owner<kSplitCtas>(s, total);
+            c0 = share_owner<kSplitCtas>(s + 1, total);
             c1 = share_owner<kSplitCtas>(s + nt - 1, total);
         }
         __syncthreads();
         if (warp < heads) {
             // (a maximum of -inf: no row, or NaN alone, which stays in the sums)
             float mx = -INFINITY, ls = 0.f;
-            for (int64_t c = c0 + lane; c <= c1; c += 32)
-                mx = fmaxf(mx, dc.part_ml[((c + unit) * dc.hg + warp) * 2]);
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            auto join = [&](float m, float l) {
+                const float top = fmaxf(mx, m);
+                ls = (mx == -INFINITY ? ls : ls * exp2f(mx - top)) + (m == -INFINITY ? l : l * exp2f(m - top));
+                mx = top;
+            };
             for (int64_t c = c0 + lane; c <= c1; c += 32) {
-                const float *ml = dc.part_ml + ((c + unit) * dc.hg + warp) * 2;
-                ls = fmaf(ml[1], mx == -INFINITY ? 0.f : exp2f(ml[0] - mx), ls);
+                const float2 ml = reinterpret_cast<const float2 *>(dc.part_ml)[(c + unit) * dc.hg + warp];
+                join(ml.x, ml.y);
             }
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, off);
+            for (int off = 16; off > 0; off >>= 1) {
+                const float m = __shfl_xor_sync(0xffffffffu, mx, off), l = __shfl_xor_sync(0xffffffffu, ls, off);
+                join(m, l);
+            }
             if (lane == 0) {
                 s_mx[warp] = mx;
                 s_il[warp] = ls == 0.f ? 0.f : 1.f / ls;
@@ -675,14 +756,16 @@ k_paged_join(const T *__restrict__ q, float *weights, T *__restrict__ out, PageA
                 }
                 reinterpret_cast<float4 *>(sq)[grp * cols + col] = y;
             }
+            __shared__ float s_gate[8];
+            if (mem && tid < heads) s_gate[tid] = 1.f / (1.f + expf(-beta));
             __syncthreads();
             for (int i = tid; i < heads * D; i += NT) {
                 const int h = i / D;
                 float y = 0.f;
                 for (int k = 0; k < groups; ++k) y += sq[k * cols * 4 + i];
                 y *= s_il[h];
-                if (dc.M) {
-                    const float gt = 1.f / (1.f + expf(-dc.beta[kvh * dc.G + ht * dc.hg + h]));
+                if (mem) {
+                    const float gt = s_gate[h];
                     const int w = dc.hg * D;
                     const float num = (s_num[i] + s_num[w + i]) + (s_num[2 * w + i] + s_num[3 * w + i]);
                     y = gt * (s_den[h] == 0.f ? 0.f : num / s_den[h]) + (1.f - gt) * y;
@@ -690,21 +773,26 @@ k_paged_join(const T *__restrict__ q, float *weights, T *__restrict__ out, PageA
                 st_f(out + (h0 + ht * dc.hg) * D + i, y);
             }
         }
-        if (weights) {
-            const int *table = a.table + b * a.max_pages;
-            for (int64_t j0 = (int64_t)blockIdx.y * kJoinRows; j0 < n; j0 += (int64_t)gridDim.y * kJoinRows)
+        if (weights)
+            for (int64_t j0 = (int64_t)blockIdx.y * kJoinRows; j0 < n; j0 += (int64_t)gridDim.y * kJoinRows) {
+                if (ht > 0 || j0 != (int64_t)blockIdx.y * kJoinRows || dc.HT > 1) load_weights(j0);
+                float sum[PER] = {};
+                for (int g = 0; g < heads; ++g) {
+                    const float mx = s_mx[g], il = s_il[g];
 #pragma unroll
-                for (int e = 0; e < kJoinRows / NT; ++e) {
-                    const int64_t j = j0 + e * NT + tid;
-                    const int64_t row = j < n ? pool_row(a, table, j, kvh) : -1;
-                    if (row < 0) continue;
-                    float sum = 0.f;
-                    const float *x = dc.scores + row * dc.G + ht * dc.hg;
-                    for (int g = 0; g < heads; ++g)
-                        sum = fmaf(s_mx[g] == -INFINITY ? 0.f : exp2f(x[g] - s_mx[g]), s_il[g], sum);
-                    weights[row] = j == len && ht == 0 ? sum : weights[row] + sum;
+                    for (int e = 0; e < PER; ++e)
+                        if (place[e] >= 0) {
+                            const float x = dc.scores[place[e] * dc.G + ht * dc.hg + g];
+                            sum[e] = fmaf(mx == -INFINITY ? 0.f : exp2f(x - mx), il, sum[e]);
+                        }
                 }
-        }
+#pragma unroll
+                for (int e = 0; e < PER; ++e)
+                    if (place[e] >= 0) {
+                        const bool later = ht > 0 && j0 + e * NT + tid == len;   // its other heads' part
+                        weights[place[e]] = (later ? weights[place[e]] : so_far[e]) + sum[e];
+                    }
+            }
     }
 }
 

@@ -6,6 +6,9 @@
 // lengths are known on the device alone, and a long sequence beside short ones leaves no SM idle.
 // A unit's part in one CTA is a piece; along the numbering each new piece has a higher CTA or a
 // higher unit, so c + unit names it uniquely (below NC + units).
+//
+// With LEAD = 1 every unit has one tile without rows before its own, which stands for what a
+// piece costs besides its rows: a CTA of many short units would end last otherwise.
 #pragma once
 
 #include <stdint.h>
@@ -36,14 +39,21 @@ __device__ __forceinline__ int64_t share_owner(int64_t t, int64_t total)
     return ((t + 1) * C - 1) / total;
 }
 
+template <int LEAD>
+__device__ __forceinline__ int64_t share_tiles(int64_t rows, int TR)
+{
+    const int64_t t = (rows + TR - 1) / TR;
+    return t > 0 ? t + LEAD : 0;
+}
+
 // Tiles per head of all sequences, and of those before sequence `want`.  The whole block calls.
-template <int NT, class Rows>
+template <int NT, int LEAD, class Rows>
 __device__ __forceinline__ int64_t share_count(const Rows &rows, int64_t B, int TR, int64_t want, ShareScratch &s,
                                                int64_t &before)
 {
     int64_t all = 0, pre = 0;
     for (int64_t b = threadIdx.x; b < B; b += NT) {
-        const int64_t t = (rows(b) + TR - 1) / TR;
+        const int64_t t = share_tiles<LEAD>(rows(b), TR);
         all += t;
         if (b < want) pre += t;
     }
@@ -75,7 +85,7 @@ struct Walk {
     int n;                       // its rows
 };
 
-template <class Rows>
+template <int LEAD, class Rows>
 __device__ __forceinline__ bool walk_next(Walk &w, const Rows &rows, int KH, int64_t B, int TR)
 {
     if (++w.tile < w.nt) return false;
@@ -84,7 +94,7 @@ __device__ __forceinline__ bool walk_next(Walk &w, const Rows &rows, int KH, int
     w.kh = 0;
     for (++w.b; w.b < B; ++w.b) {
         w.n = (int)rows(w.b);
-        w.nt = (w.n + TR - 1) / TR;
+        w.nt = (int)share_tiles<LEAD>(w.n, TR);
         if (w.nt > 0) break;
     }
     return true;
@@ -92,19 +102,19 @@ __device__ __forceinline__ bool walk_next(Walk &w, const Rows &rows, int KH, int
 
 // This CTA's tiles [t0, t1) and where the first one lies.  The whole block calls; with t0 >= t1
 // there is nothing to do.
-template <int NC, int NT, class Rows>
+template <int NC, int NT, int LEAD, class Rows>
 __device__ __forceinline__ void share_begin(const Rows &rows, int64_t B, int KH, int TR, ShareScratch &s, int64_t &t0,
                                             int64_t &t1, Walk &w)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t total = 0, none;
     const bool few = B <= NT;            // one look at the lengths serves both passes
-    if (!few) total = KH * share_count<NT>(rows, B, TR, 0, s, none);
+    if (!few) total = KH * share_count<NT, LEAD>(rows, B, TR, 0, s, none);
     t0 = t1 = 0;
     int64_t base = 0, at = 0;
     for (int64_t b0 = 0; b0 < B; b0 += NT) {
         const int64_t b = b0 + threadIdx.x;
-        const int64_t mine = b < B ? (rows(b) + TR - 1) / TR : 0;
+        const int64_t mine = b < B ? share_tiles<LEAD>(rows(b), TR) : 0;
         int64_t inc = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -137,7 +147,7 @@ __device__ __forceinline__ void share_begin(const Rows &rows, int64_t B, int KH,
     }
     w.b = (int)s.b;
     w.n = (int)rows(w.b);
-    w.nt = (w.n + TR - 1) / TR;
+    w.nt = (int)share_tiles<LEAD>(w.n, TR);
     const int64_t in_b = t0 - s.before * KH;
     w.kh = (int)(in_b / w.nt);
     w.tile = (int)(in_b % w.nt);
