@@ -281,7 +281,7 @@ k_evict_move(T *k_pages, T *v_pages, float *weights, PageArgs a, EvictArgs e, in
 // one unit per addition, all in one direction.
 //
 // The evicted rows of all heads are shared out evenly over 148 CTAs (share.cuh).  In each, 16
-// loader warps keep a stage of rows in flight in registers, form sigma and the parts and sum z;
+// loader warps copy rows two stages ahead (64 KB in flight), form sigma and the parts and sum z;
 // one thread issues the products; eight warps read the accumulators.  Reading K and V is the
 // bound (4 d bytes a row against 2 d^2 operations); the parts' products are a quarter of the
 // tensor rate at that speed.
@@ -289,19 +289,24 @@ constexpr int kFoldCtas = 148;
 constexpr int kFoldLoaders = 16, kFoldReaders = 8;
 constexpr int kFoldThreads = 32 * (kFoldLoaders + kFoldReaders + 4);
 constexpr int kFoldRows = 128;       // rows of a tile: one reading of the accumulators
-constexpr int kFoldHalf = 64;        // rows of a stage
 
 template <typename T, int D>
 struct FoldTile {
     static constexpr bool kWide = sizeof(T) == 4;
     static constexpr int VP = kWide ? 3 : 1;               // parts of v
-    static constexpr int KB = 2 * kFoldHalf * 128;         // bytes of a part: two blocks of 64 columns
-    static constexpr int LR = kFoldHalf / kFoldLoaders;    // rows of a loader warp
-    static constexpr int STAGE = (3 + VP) * KB;
-    static constexpr int STAGES = kWide ? 2 : 3;
-    static constexpr int SMEM = STAGES * STAGE + 1024;     // rounded up to 1024 inside
+    static constexpr int HALF = kWide ? 32 : 64;           // rows of a stage
+    static constexpr int SUB = kFoldRows / HALF;           // stages of a tile
+    static constexpr int KB = 2 * HALF * 128;              // bytes of a part: two blocks of 64 columns
+    // Staged parts, two deep (fp32: v's parts with them; bf16: v as it is, four deep), then the
+    // rows as they arrive, three deep.
+    static constexpr int PART = kWide ? 6 * KB : 3 * KB;
     static constexpr int CPR = D * (int)sizeof(T) / 16;    // 16-byte chunks of a row
-    static constexpr int LD = (LR * CPR + 31) / 32;   // chunks per lane, tensor and step
+    static constexpr int LR = HALF / kFoldLoaders;         // rows of a loader warp and stage
+    static constexpr int LD = (LR * CPR + 31) / 32;        // chunks per lane, tensor and stage
+    static constexpr int RAW = kFoldLoaders * LD * 512 * (kWide ? 2 : 1);   // a chunk's place per lane
+    static constexpr int V_AT = 2 * PART, RAW_AT = V_AT + (kWide ? 0 : 4 * KB);
+    static constexpr int SMEM = RAW_AT + 3 * RAW + 1024;   // rounded up to 1024 inside
+    static_assert(SMEM <= 227 * 1024, "shared memory");
     static constexpr int E = 16 / (int)sizeof(T);          // channels of a chunk
     static constexpr uint32_t COLS = 4 * D;                // two buffers of two accumulators
 };
@@ -336,7 +341,7 @@ __global__ void __launch_bounds__(kFoldThreads, 1)
 k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageArgs a, EvictArgs e, float *M)
 {
     using Tile = FoldTile<T, D>;
-    constexpr int CPR = Tile::CPR, LD = Tile::LD, E = Tile::E, ST = Tile::STAGES, VP = Tile::VP;
+    constexpr int CPR = Tile::CPR, LD = Tile::LD, E = Tile::E, SUB = Tile::SUB, HALF = Tile::HALF, VP = Tile::VP, ST = 2;
     extern __shared__ unsigned char s_raw[];
     __shared__ __align__(8) uint64_t full[ST], empty[ST], tfull[2], tempty[2];
     __shared__ uint32_t s_tmem;
@@ -366,7 +371,7 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
         tc::fence_barrier_init();
     }
     if (D < 128)                        // columns that no row fills: features past D are 0
-        for (int i = tid; i < ST * Tile::STAGE / 16; i += kFoldThreads)
+        for (int i = tid; i < Tile::RAW_AT / 16; i += kFoldThreads)
             reinterpret_cast<uint4 *>(base)[i] = make_uint4(0, 0, 0, 0);
     if (warp == 0) tc::tmem_alloc(&s_tmem, Tile::COLS);
     tc::fence_proxy_async_smem();
@@ -379,8 +384,8 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
 
     if (warp < kFoldLoaders) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        // Lanes 0-3 look up this warp's rows of a tile's first half, 4-7 those of the second: the
-        // evicted row's number three tiles ahead, its page two, its data one stage.
+        // Lane x looks up row x % LR of this warp in stage x / LR of a tile: the evicted row's number
+        // two tiles ahead, its page one, its data two stages.
         constexpr int LR = Tile::LR;
         Walk ahead = first;
         int64_t t_ahead = t1 - t0;
@@ -389,10 +394,10 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
         auto take_row = [&] {
             r1 = -1;
             if (t_ahead <= 0) return;
-            const int j = ahead.tile * kFoldRows + lane / LR * kFoldHalf + warp * LR + lane % LR;
+            const int j = ahead.tile * kFoldRows + lane / LR * HALF + warp * LR + lane % LR;
             b1 = ahead.b;
             kvh1 = ahead.kh;
-            if (lane < 2 * LR && j < ahead.n) r1 = e.gone[((int64_t)b1 * a.Hkv + kvh1) * e.gone_stride + j];
+            if (lane < SUB * LR && j < ahead.n) r1 = e.gone[((int64_t)b1 * a.Hkv + kvh1) * e.gone_stride + j];
             walk_next<0>(ahead, rows_of, a.Hkv, e.B, kFoldRows);
             --t_ahead;
         };
@@ -414,90 +419,111 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
                     g_page_status = 1;
             }
         };
-        uint4 rk[LD], rv[LD];
-        uint32_t ok = 0;                // bit i: chunk i is a row's
-        // chunk i of a stage: row ci / CPR of this warp's, column ci % CPR (the same in every stage)
-        auto load = [&](int i, int h) {
-            const int ci = i * 32 + lane;
-            const int64_t at = __shfl_sync(0xffffffffu, base3, h * LR + (ci / CPR) % LR);
-            const bool on = at >= 0 && ci < LR * CPR;
-            rk[i] = rv[i] = make_uint4(0, 0, 0, 0);
-            if (on) {
-                rk[i] = __ldcs(reinterpret_cast<const uint4 *>(k_pages) + at * CPR + ci % CPR);
-                rv[i] = __ldcs(reinterpret_cast<const uint4 *>(v_pages) + at * CPR + ci % CPR);
-            }
-            ok = on ? ok | 1u << i : ok & ~(1u << i);
-        };
-        take_row();
-        take_page();
-        take_row();
-        take_base();
-        take_page();
-        take_row();
+        // Chunk i of a stage: row ci / CPR of this warp, column ci % CPR (the same in every stage);
+        // a lane converts what it copied itself.  In a part: the column block, then the row's
+        // swizzled 16-byte chunk of 8 channels.
+        uint32_t spot[LD];
 #pragma unroll
-        for (int i = 0; i < LD; ++i) load(i, 0);
+        for (int i = 0; i < LD; ++i) {
+            const int ci = i * 32 + lane, r = warp * LR + ci / CPR, ch = ci % CPR * E;
+            spot[i] = (ch >> 6) * (HALF * 128) + r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4) + (ch & 7) * 2;
+        }
+        unsigned char *raw = base + Tile::RAW_AT + (warp * LD * 32 + lane) * 16;
+        uint32_t ok = 0;                // bit 8 (stage % 4) + i: chunk i of a stage is a row's
+        // stage q (h-th of its tile) into raw slot `slot`
+        auto issue = [&](int h, int slot, uint32_t q) {
+            if (h == 0) {
+                take_base();
+                take_page();
+                take_row();
+            }
+            const uint32_t bit = (q & 3) * 8;
+            ok &= ~(0xffu << bit);
+#pragma unroll
+            for (int i = 0; i < LD; ++i) {
+                const int ci = i * 32 + lane;
+                const int64_t at = __shfl_sync(0xffffffffu, base3, h * LR + (ci / CPR) % LR);
+                if (ci < LR * CPR) {
+                    const bool on = at >= 0;
+                    const int64_t off = ((on ? at : 0) * CPR + ci % CPR) * 16;
+                    cp16(tc::smem_u32(raw + slot * Tile::RAW + i * 512),
+                         reinterpret_cast<const char *>(k_pages) + off, on);
+                    const uint32_t dv = Tile::kWide ? tc::smem_u32(raw + slot * Tile::RAW + Tile::RAW / 2 + i * 512)
+                                                    : tc::smem_u32(base + Tile::V_AT + (q & 3) * Tile::KB + spot[i]);
+                    cp16(dv, reinterpret_cast<const char *>(v_pages) + off, on);
+                    ok |= (on ? 1u : 0u) << (bit + i);
+                }
+            }
+        };
+        auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+        take_row();
+        take_page();
+        take_row();
+        const int64_t stages = steps * SUB;
+        issue(0, 0, 0);
+        commit();
+        issue(1, 1, 1);                 // (SUB >= 2)
+        commit();
         uint64_t zs[E / 2];
 #pragma unroll
         for (int x = 0; x < E / 2; ++x) zs[x] = 0;
         Walk at = first;
-        int stage = 0;
-        uint32_t lap = 0;
+        int slot = 0;                   // s % 3
+        uint32_t s = 0;                 // low bits of the stage's number
         bool alive = true;
-        for (int64_t left = t1 - t0; left > 0 && alive; --left) {
+        int64_t rest = stages;
+        for (int64_t left = steps; left > 0 && alive; --left) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (lap > 0 && alive) alive = tc::mbar_wait(&empty[stage], (lap - 1) & 1, abort, 90);
-                if (h == 1) {           // what is loaded from here on is the next tile's first half
-                    take_base();
-                    take_page();
-                    take_row();
-                }
-                unsigned char *sk = base + stage * Tile::STAGE, *sv = sk + 3 * Tile::KB;
+            for (int h = 0; h < SUB; ++h, ++s, --rest) {
+                // the products of stage s - 2 are done: its parts and its v are free
+                const int stage = s & 1;
+                if (rest <= stages - 2 && alive) alive = tc::mbar_wait(&empty[stage], ((s >> 1) - 1) & 1, abort, 90);
+                if (rest > 2) issue((h + 2) % SUB, slot == 0 ? 2 : slot - 1, s + 2);
+                commit();
+                asm volatile("cp.async.wait_group 2;" ::: "memory");
+                unsigned char *sk = base + stage * Tile::PART, *sv = sk + 3 * Tile::KB;
+                const uint32_t on_bits = ok >> ((s & 3) * 8);
 #pragma unroll
                 for (int i = 0; i < LD; ++i) {
-                    const int ci = i * 32 + lane, r = warp * LR + ci / CPR, ch = ci % CPR * E;   // row, first channel
-                    // column block, then the row's swizzled 16-byte chunk of 8 channels
-                    const uint32_t dst = (ch >> 6) * (kFoldHalf * 128) + r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4) +
-                                         (ch & 7) * 2;
-                    const bool on = ok >> i & 1, mine = ci < LR * CPR;
-                    const uint32_t w[4] = {rk[i].x, rk[i].y, rk[i].z, rk[i].w};
+                    const unsigned char *src = raw + slot * Tile::RAW + i * 512;
+                    uint4 rk = *reinterpret_cast<const uint4 *>(src);
+                    if (!(on_bits >> i & 1)) {             // no row: sigma(-inf) = 0
+                        const uint32_t none = Tile::kWide ? 0xff800000u : 0xff80ff80u;
+                        rk = make_uint4(none, none, none, none);
+                    }
+                    const uint32_t w[4] = {rk.x, rk.y, rk.z, rk.w};
                     uint32_t p[E / 2][3];
 #pragma unroll
                     for (int x = 0; x < E / 2; ++x) {
                         uint64_t f;
                         if constexpr (Tile::kWide) f = sigma2(__uint_as_float(w[2 * x]), __uint_as_float(w[2 * x + 1]));
                         else f = sigma2(__uint_as_float(w[x] << 16), __uint_as_float(w[x] & 0xffff0000u));
-                        f = on ? f : 0;
                         zs[x] = tc::f2_add(zs[x], f);
                         split3(f, p[x]);
                     }
-                    if (mine) {
+                    if (i * 32 + lane < LR * CPR) {
                         if constexpr (!Tile::kWide) {
 #pragma unroll
                             for (int y = 0; y < 3; ++y)
-                                *reinterpret_cast<uint4 *>(sk + y * Tile::KB + dst) =
+                                *reinterpret_cast<uint4 *>(sk + y * Tile::KB + spot[i]) =
                                     make_uint4(p[0][y], p[1][y], p[2][y], p[3][y]);
-                            *reinterpret_cast<uint4 *>(sv + dst) = rv[i];
                         } else {
+                            const uint4 rv = *reinterpret_cast<const uint4 *>(src + Tile::RAW / 2);
                             uint32_t q[2][3];
-                            split3(tc::f2_pack(__uint_as_float(rv[i].x), __uint_as_float(rv[i].y)), q[0]);
-                            split3(tc::f2_pack(__uint_as_float(rv[i].z), __uint_as_float(rv[i].w)), q[1]);
+                            split3(tc::f2_pack(__uint_as_float(rv.x), __uint_as_float(rv.y)), q[0]);
+                            split3(tc::f2_pack(__uint_as_float(rv.z), __uint_as_float(rv.w)), q[1]);
 #pragma unroll
                             for (int y = 0; y < 3; ++y) {
-                                *reinterpret_cast<uint2 *>(sk + y * Tile::KB + dst) = make_uint2(p[0][y], p[1][y]);
-                                *reinterpret_cast<uint2 *>(sv + y * Tile::KB + dst) = make_uint2(q[0][y], q[1][y]);
+                                *reinterpret_cast<uint2 *>(sk + y * Tile::KB + spot[i]) = make_uint2(p[0][y], p[1][y]);
+                                *reinterpret_cast<uint2 *>(sv + y * Tile::KB + spot[i]) = make_uint2(q[0][y], q[1][y]);
                             }
                         }
                     }
-                    load(i, h ^ 1);     // the next stage's chunk into the registers just read
                 }
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&full[stage]);
-                if (++stage == ST) {
-                    stage = 0;
-                    ++lap;
-                }
+                slot = slot == 2 ? 0 : slot + 1;
             }
             if (left == 1 || at.tile == at.nt - 1) {   // a piece ends: this warp's part of z
                 const int64_t slot = blockIdx.x + (int64_t)at.b * a.Hkv + at.kh;
@@ -520,6 +546,7 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
             }
             walk_next<0>(at, rows_of, a.Hkv, e.B, kFoldRows);
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
     } else if (warp < kFoldLoaders + kFoldReaders) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         // reader w: lanes 32 (w % 4) .. + 31 (key features), half w / 4 of the columns
@@ -583,25 +610,26 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
       asm volatile("setmaxnreg.dec.sync.aligned.u32 24;");
       if (warp == kFoldLoaders + kFoldReaders && lane == 0) {
         constexpr uint32_t idesc = tc::idesc_bf16(128, D, 1, 1);
-        int stage = 0;
-        uint32_t lap = 0;
+        uint32_t q = 0;                 // the stage's number
         for (int64_t s = 0; s < steps; ++s) {
             const int buf = (int)(s & 1);
             if (s >= 2 && !tc::mbar_wait(&tempty[buf], (uint32_t)(((s >> 1) - 1) & 1), abort, 92)) break;
             const uint32_t d0 = tmem + buf * 2 * D, d1 = d0 + D;
-            for (int h = 0; h < 2; ++h) {
-                if (!tc::mbar_wait(&full[stage], lap & 1, abort, 93)) break;
+            for (int h = 0; h < SUB; ++h, ++q) {
+                if (!tc::mbar_wait(&full[q & 1], (q >> 1) & 1, abort, 93)) break;
                 tc::tc_fence_after();
-                const uint32_t sk = tc::smem_u32(base + stage * Tile::STAGE), sv = sk + 3 * Tile::KB;
+                const uint32_t sk = tc::smem_u32(base + (q & 1) * Tile::PART);
+                const uint32_t sv = Tile::kWide ? sk + 3 * Tile::KB
+                                                : tc::smem_u32(base + Tile::V_AT + (q & 3) * Tile::KB);
                 uint32_t on = h;
 #pragma unroll
                 for (int i = 0; i < 3; ++i)
 #pragma unroll
                     for (int j = 0; j < VP; ++j) {
                         if (i + j > 2) continue;
-                        for (int kk = 0; kk < kFoldHalf / 16; ++kk) {
-                            const uint64_t da = tc::sdesc_sw128(sk + i * Tile::KB + kk * 2048, kFoldHalf * 128, 1024);
-                            const uint64_t db = tc::sdesc_sw128(sv + j * Tile::KB + kk * 2048, kFoldHalf * 128, 1024);
+                        for (int kk = 0; kk < HALF / 16; ++kk) {
+                            const uint64_t da = tc::sdesc_sw128(sk + i * Tile::KB + kk * 2048, HALF * 128, 1024);
+                            const uint64_t db = tc::sdesc_sw128(sv + j * Tile::KB + kk * 2048, HALF * 128, 1024);
                             if (i + j == 0) {
                                 tc::mma_ss(d0, da, db, idesc, h + kk > 0);
                             } else {
@@ -610,11 +638,7 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
                             }
                         }
                     }
-                tc::mma_commit(&empty[stage]);
-                if (++stage == ST) {
-                    stage = 0;
-                    ++lap;
-                }
+                tc::mma_commit(&empty[q & 1]);
             }
             tc::mma_commit(&tfull[buf]);
         }
@@ -647,30 +671,31 @@ k_evict_reduce(PageArgs a, EvictArgs e, float *M, float *z)
     const int64_t total = a.Hkv * share_count<256, 0>(rows_of, e.B, kFoldRows, b, s_share, before);
     const int64_t s = before * a.Hkv + kvh * nt;
     const int64_t c0 = share_owner<kFoldCtas>(s, total), c1 = share_owner<kFoldCtas>(s + nt - 1, total);
-    if (c0 != c1) {
-        const int i = blockIdx.y * 256 + threadIdx.x;      // [c / 4][f]
+    const int i = blockIdx.y * 256 + threadIdx.x;          // [c / 4][f]
+    if (c0 != c1 && i < D * D / 4) {
         const int f = i % D, c4 = i / D;
         const float4 *p = reinterpret_cast<const float4 *>(e.part_M);
+        float4 *dst = reinterpret_cast<float4 *>(M) + (unit * D + f) * (D / 4) + c4;
+        const float4 old = *dst;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
         for (int64_t c = c0; c <= c1; ++c) {
             const float4 y = p[(c + unit) * (D * D / 4) + i];
             x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
         }
-        float4 *dst = reinterpret_cast<float4 *>(M) + (unit * D + f) * (D / 4) + c4;
-        const float4 y = *dst;
-        *dst = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+        *dst = make_float4(x.x + old.x, x.y + old.y, x.z + old.z, x.w + old.w);
     }
-    if (blockIdx.y == 0 && threadIdx.x < D) {
+    // z: a warp per feature, its lanes over the pieces' loader warps
+    const int per = D / gridDim.y, lane = threadIdx.x & 31;
+    for (int k = threadIdx.x / 32; k < per; k += 8) {
+        const int f = blockIdx.y * per + k;
+        const float *p = e.part_z + (c0 + unit) * kFoldLoaders * D + f;
         float x = 0.f;
-        for (int64_t c = c0; c <= c1; ++c) {
-            const float *p = e.part_z + (c + unit) * kFoldLoaders * D + threadIdx.x;
-            float y = 0.f;
+#pragma unroll 4
+        for (int64_t w = lane; w < (c1 - c0 + 1) * kFoldLoaders; w += 32) x += p[w * D];
 #pragma unroll
-            for (int w = 0; w < kFoldLoaders; ++w) y += p[w * D];
-            x += y;
-        }
-        z[unit * D + threadIdx.x] += x;
+        for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+        if (lane == 0) z[unit * D + f] += x;
     }
 }
 

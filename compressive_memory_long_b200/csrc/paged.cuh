@@ -45,6 +45,15 @@ __device__ __forceinline__ int64_t pool_row(const PageArgs &a, const int *table_
     return ((((int64_t)pg * a.Hkv + kvh) << a.shift) | (r & (((int64_t)1 << a.shift) - 1)));
 }
 
+__device__ __forceinline__ uint32_t s_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// 16 bytes global -> shared, zeros where !ok (the source is not read then).
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok)
+{
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
+                 : "memory");
+}
+
 // A block's rows when 16 bytes go to a thread and row: four rows of keys and values in flight.
 template <typename T, int D>
 struct RowTile {
