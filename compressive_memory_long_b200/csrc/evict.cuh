@@ -103,8 +103,9 @@ k_evict_select(const float *__restrict__ weights, PageArgs a, EvictArgs e, int C
     const int old = n - min(e.recent, n), m = e.budget - (n - old);   // keep m of rows 0..old-1
     for (int i = rank * NT + tid; i < n - old; i += CS * NT) kept[m + i] = old + i;
     const int per = (old + CS - 1) / CS, r0 = min(rank * per, old), cnt = min(per, old - r0);
-    auto load_key = [&](int i) {
-        const int64_t row = pool_row(a, table, r0 + i, kvh);
+    bool bad = false;
+    auto load_key = [&](int i) {        // a row without a page goes first
+        const int64_t row = place_of(a, table, r0 + i, kvh, bad);
         return row < 0 ? 0u : weight_key(__ldcs(weights + row));
     };
     auto key_of = [&](int i) { return i < cap ? keys[i] : load_key(i); };
@@ -215,59 +216,8 @@ k_evict_select(const float *__restrict__ weights, PageArgs a, EvictArgs e, int C
         gt += __popc(bg);
         eq += __popc(be);
     }
+    report(bad);
     if (CS > 1) cluster_sync();         // no CTA leaves while another reads its counts
-}
-
-// ---- move ---------------------------------------------------------------------------------------
-//
-// Copies the kept rows: 16 bytes per thread and row, four rows of keys and values in flight each.
-template <typename T, int D>
-__global__ void __launch_bounds__(256)
-k_evict_move(T *k_pages, T *v_pages, float *weights, PageArgs a, EvictArgs e, int blocks)
-{
-    using Tile = RowTile<T, D>;
-    constexpr int CPR = Tile::CPR, LINES = Tile::LINES, ROWS = Tile::ROWS;
-    __shared__ int64_t s_from[ROWS], s_to[ROWS];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t unit = blockIdx.x / blocks, b = unit / a.Hkv;
-    const int j0 = (int)(blockIdx.x % blocks) * ROWS;
-    const int kvh = (int)(unit % a.Hkv), n = min(cached_rows(a, b), e.budget), tid = threadIdx.x;
-    if (j0 >= n) return;
-    PageArgs dst = a;
-    dst.table = e.dst_table;
-    dst.max_pages = e.dst_pages;
-    for (int i = tid; i < ROWS; i += 256) {
-        int64_t from = -1, to = -1;
-        if (j0 + i < n) {
-            from = pool_row(a, a.table + b * a.max_pages, e.kept[unit * e.budget + j0 + i], kvh);
-            to = pool_row(dst, e.dst_table + b * e.dst_pages, j0 + i, kvh);
-            if (from < 0 || to < 0 || from == to) from = -1;
-            else weights[to] = weights[from];
-        }
-        s_from[i] = from;
-        s_to[i] = to;
-    }
-    __syncthreads();
-    const int c = tid % CPR, line = tid / CPR;
-    uint4 *kp = reinterpret_cast<uint4 *>(k_pages), *vp = reinterpret_cast<uint4 *>(v_pages);
-    uint4 x[4], y[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const int64_t from = s_from[line + u * LINES];
-        if (from >= 0) {
-            x[u] = __ldcs(kp + from * CPR + c);
-            y[u] = __ldcs(vp + from * CPR + c);
-        }
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const int64_t to = s_to[line + u * LINES];
-        if (s_from[line + u * LINES] >= 0) {
-            kp[to * CPR + c] = x[u];
-            vp[to * CPR + c] = y[u];
-        }
-    }
 }
 
 // ---- fold ---------------------------------------------------------------------------------------
@@ -276,7 +226,7 @@ k_evict_move(T *k_pages, T *v_pages, float *weights, PageArgs a, EvictArgs e, in
 // B = V (N = the value features), both staged row by row (MN-major), 64 rows a stage.  M and z are
 // 32-bit sums, so sigma(k) is split into three bf16 parts (24 bits; two would leave 2^-18, more
 // than the sum's own rounding), v into one (bf16, exact) or three (fp32: the six products down to
-// 2^-24 are kept).  The leading product has an accumulator of its own and every 128 rows' result is
+// 2^-24 are kept).  The leading product has an accumulator of its own and every 256 rows' result is
 // read out and added in registers: the tensor core's own additions over a long axis lose about
 // one unit per addition, all in one direction.
 //
@@ -288,7 +238,7 @@ k_evict_move(T *k_pages, T *v_pages, float *weights, PageArgs a, EvictArgs e, in
 constexpr int kFoldCtas = 148;
 constexpr int kFoldLoaders = 16, kFoldReaders = 8;
 constexpr int kFoldThreads = 32 * (kFoldLoaders + kFoldReaders + 4);
-constexpr int kFoldRows = 128;       // rows of a tile: one reading of the accumulators
+constexpr int kFoldRows = 256;       // rows of a tile: one reading of the accumulators
 
 template <typename T, int D>
 struct FoldTile {
@@ -350,13 +300,15 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
     unsigned char *base = s_raw + ((1024 - (tc::smem_u32(s_raw) & 1023)) & 1023);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
 
     auto rows_of = [&](int64_t b) { return (int64_t)max(0, cached_rows(a, b) - e.budget); };
     Walk first;
     int64_t t0, t1;
     share_begin<kFoldCtas, kFoldThreads, 0>(rows_of, e.B, a.Hkv, kFoldRows, s_share, t0, t1, first);
-    if (t0 >= t1) return;               // the whole CTA
+    if (t0 >= t1) {                     // the whole CTA
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
 
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
@@ -376,6 +328,7 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
     if (warp == 0) tc::tmem_alloc(&s_tmem, Tile::COLS);
     tc::fence_proxy_async_smem();
     tc::tc_fence_before();
+    asm volatile("griddepcontrol.wait;" ::: "memory");     // from here on the selection is read, M written
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = s_tmem;
@@ -429,7 +382,8 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
             spot[i] = (ch >> 6) * (HALF * 128) + r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4) + (ch & 7) * 2;
         }
         unsigned char *raw = base + Tile::RAW_AT + (warp * LD * 32 + lane) * 16;
-        uint32_t ok = 0;                // bit 8 (stage % 4) + i: chunk i of a stage is a row's
+        uint32_t ok = 0;                // bit 8 (stage % 4) + i: chunk i of a stage is a row's;
+                                        // bit 7 of them: so are all of this warp's
         // stage q (h-th of its tile) into raw slot `slot`
         auto issue = [&](int h, int slot, uint32_t q) {
             if (h == 0) {
@@ -439,6 +393,9 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
             }
             const uint32_t bit = (q & 3) * 8;
             ok &= ~(0xffu << bit);
+            const bool all = (__ballot_sync(0xffffffffu, base3 >= 0) >> (h * LR) & ((1u << LR) - 1)) == (1u << LR) - 1 &&
+                             LR * CPR >= 32;
+            if (all) ok |= 0x80u << bit;
 #pragma unroll
             for (int i = 0; i < LD; ++i) {
                 const int ci = i * 32 + lane;
@@ -451,7 +408,7 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
                     const uint32_t dv = Tile::kWide ? tc::smem_u32(raw + slot * Tile::RAW + Tile::RAW / 2 + i * 512)
                                                     : tc::smem_u32(base + Tile::V_AT + (q & 3) * Tile::KB + spot[i]);
                     cp16(dv, reinterpret_cast<const char *>(v_pages) + off, on);
-                    ok |= (on ? 1u : 0u) << (bit + i);
+                    if (!all) ok |= (on ? 1u : 0u) << (bit + i);
                 }
             }
         };
@@ -487,7 +444,7 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
                 for (int i = 0; i < LD; ++i) {
                     const unsigned char *src = raw + slot * Tile::RAW + i * 512;
                     uint4 rk = *reinterpret_cast<const uint4 *>(src);
-                    if (!(on_bits >> i & 1)) {             // no row: sigma(-inf) = 0
+                    if (!(on_bits >> 7 & 1) && !(on_bits >> i & 1)) {   // no row: sigma(-inf) = 0
                         const uint32_t none = Tile::kWide ? 0xff800000u : 0xff80ff80u;
                         rk = make_uint4(none, none, none, none);
                     }
@@ -654,49 +611,138 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
     if (warp == 0) tc::tmem_dealloc(tmem, Tile::COLS);
 }
 
-// The pieces of a head that several CTAs folded, in order, into its memory; z of every head.
-template <int D>
-__global__ void __launch_bounds__(256)
-k_evict_reduce(PageArgs a, EvictArgs e, float *M, float *z)
+// ---- finish -------------------------------------------------------------------------------------
+//
+// One grid for what is left: blocks that copy the kept rows (16 bytes per thread and row, four
+// rows of keys and values in flight), and with a memory blocks that add the pieces of a head that
+// several CTAs folded, in order, and z of every head.
+template <typename T, int D>
+__device__ __forceinline__ void move_rows(T *k_pages, T *v_pages, float *weights, const PageArgs &a, const EvictArgs &e,
+                                          int64_t block, int blocks)
 {
-    __shared__ ShareScratch s_share;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t unit = blockIdx.x, b = unit / a.Hkv;
-    const int kvh = (int)(unit % a.Hkv);
-    auto rows_of = [&](int64_t i) { return (int64_t)max(0, cached_rows(a, i) - e.budget); };
-    const int64_t n = rows_of(b), nt = (n + kFoldRows - 1) / kFoldRows;
-    if (n == 0) return;
-    int64_t before;
-    const int64_t total = a.Hkv * share_count<256, 0>(rows_of, e.B, kFoldRows, b, s_share, before);
-    const int64_t s = before * a.Hkv + kvh * nt;
-    const int64_t c0 = share_owner<kFoldCtas>(s, total), c1 = share_owner<kFoldCtas>(s + nt - 1, total);
-    const int i = blockIdx.y * 256 + threadIdx.x;          // [c / 4][f]
-    if (c0 != c1 && i < D * D / 4) {
-        const int f = i % D, c4 = i / D;
-        const float4 *p = reinterpret_cast<const float4 *>(e.part_M);
-        float4 *dst = reinterpret_cast<float4 *>(M) + (unit * D + f) * (D / 4) + c4;
-        const float4 old = *dst;
+    using Tile = RowTile<T, D>;
+    constexpr int CPR = Tile::CPR, LINES = Tile::LINES, ROWS = Tile::ROWS;
+    __shared__ int64_t s_from[ROWS], s_to[ROWS];
+    const int64_t unit = block / blocks, b = unit / a.Hkv;
+    const int j0 = (int)(block % blocks) * ROWS;
+    const int kvh = (int)(unit % a.Hkv), n = min(cached_rows(a, b), e.budget), tid = threadIdx.x;
+    if (j0 >= n) return;
+    PageArgs dst = a;
+    dst.table = e.dst_table;
+    dst.max_pages = e.dst_pages;
+    bool bad = false;
+    for (int i = tid; i < ROWS; i += 256) {
+        int64_t from = -1, to = -1;
+        if (j0 + i < n) {
+            to = place_of(dst, e.dst_table + b * e.dst_pages, j0 + i, kvh, bad);
+            from = place_of(a, a.table + b * a.max_pages, e.kept[unit * e.budget + j0 + i], kvh, bad);
+            if (from < 0 || to < 0 || from == to) from = -1;
+            else weights[to] = weights[from];
+        }
+        s_from[i] = from;
+        s_to[i] = to;
+    }
+    report(bad);
+    __syncthreads();
+    const int c = tid % CPR, line = tid / CPR;
+    uint4 *kp = reinterpret_cast<uint4 *>(k_pages), *vp = reinterpret_cast<uint4 *>(v_pages);
+    uint4 x[4], y[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int64_t from = s_from[line + u * LINES];
+        if (from >= 0) {
+            x[u] = __ldcs(kp + from * CPR + c);
+            y[u] = __ldcs(vp + from * CPR + c);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int64_t to = s_to[line + u * LINES];
+        if (s_from[line + u * LINES] >= 0) {
+            kp[to * CPR + c] = x[u];
+            vp[to * CPR + c] = y[u];
+        }
+    }
+}
+
+// Block `part` of `parts` of a head: its share of M's float4 columns (32 at a time, eight warps
+// over the pieces), the last block z (a warp per eighth of the pieces' loader warps).
+template <int D>
+__device__ __forceinline__ void add_pieces(const PageArgs &a, const EvictArgs &e, float *M, float *z, int64_t unit,
+                                           int64_t c0, int64_t c1, int part, int parts)
+{
+    __shared__ float4 s_sum[256];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto total = [&](float4 x) {         // over the eight warps; lane's sum, in warp 0
+        s_sum[threadIdx.x] = x;
+        __syncthreads();
+        if (warp == 0)
+#pragma unroll
+            for (int w = 1; w < 8; ++w) {
+                const float4 y = s_sum[w * 32 + lane];
+                x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+            }
+        __syncthreads();
+        return x;
+    };
+    if (part == parts - 1) {
+        const float4 *p = reinterpret_cast<const float4 *>(e.part_z) + (c0 + unit) * kFoldLoaders * (D / 4);
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (lane < D / 4)
 #pragma unroll 8
-        for (int64_t c = c0; c <= c1; ++c) {
-            const float4 y = p[(c + unit) * (D * D / 4) + i];
+            for (int64_t w = warp; w < (c1 - c0 + 1) * kFoldLoaders; w += 8) {
+                const float4 y = p[w * (D / 4) + lane];
+                x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+            }
+        x = total(x);
+        if (warp == 0 && lane < D / 4) {
+            float4 *dst = reinterpret_cast<float4 *>(z + unit * D) + lane;
+            const float4 y = *dst;
+            *dst = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+        }
+        return;
+    }
+    if (c0 == c1) return;                // folded in place
+    for (int i0 = part * 32; i0 < D * D / 4; i0 += (parts - 1) * 32) {
+        const int i = i0 + lane, f = i % D, c4 = i / D;    // [c / 4][f]
+        const float4 *p = reinterpret_cast<const float4 *>(e.part_M) + i;
+        float4 *dst = reinterpret_cast<float4 *>(M) + (unit * D + f) * (D / 4) + c4;
+        float4 old = make_float4(0.f, 0.f, 0.f, 0.f), x = old;
+        if (warp == 0) old = *dst;
+#pragma unroll 4
+        for (int64_t c = c0 + warp; c <= c1; c += 8) {
+            const float4 y = p[(c + unit) * (D * D / 4)];
             x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
         }
-        *dst = make_float4(x.x + old.x, x.y + old.y, x.z + old.z, x.w + old.w);
+        x = total(x);
+        if (warp == 0) *dst = make_float4(x.x + old.x, x.y + old.y, x.z + old.z, x.w + old.w);
     }
-    // z: a warp per feature, its lanes over the pieces' loader warps
-    const int per = D / gridDim.y, lane = threadIdx.x & 31;
-    for (int k = threadIdx.x / 32; k < per; k += 8) {
-        const int f = blockIdx.y * per + k;
-        const float *p = e.part_z + (c0 + unit) * kFoldLoaders * D + f;
-        float x = 0.f;
-#pragma unroll 4
-        for (int64_t w = lane; w < (c1 - c0 + 1) * kFoldLoaders; w += 32) x += p[w * D];
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-        if (lane == 0) z[unit * D + f] += x;
+}
+
+// Blocks 0 .. units * parts - 1 add, the others move (parts = 0: no memory).
+template <typename T, int D>
+__global__ void __launch_bounds__(256)
+k_evict_finish(T *k_pages, T *v_pages, float *weights, PageArgs a, EvictArgs e, float *M, float *z, int64_t units,
+               int parts, int blocks)
+{
+    __shared__ ShareScratch s_share;
+    const int64_t adders = units * parts;
+    if (blockIdx.x < adders) {
+        const int64_t unit = blockIdx.x / parts, b = unit / a.Hkv;
+        const int kvh = (int)(unit % a.Hkv);
+        auto rows_of = [&](int64_t i) { return (int64_t)max(0, cached_rows(a, i) - e.budget); };
+        const int64_t nt = share_tiles<0>(rows_of(b), kFoldRows);
+        int64_t before;
+        const int64_t total = a.Hkv * share_count<256, 0>(rows_of, e.B, kFoldRows, b, s_share, before);
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (nt == 0) return;
+        const int64_t s = before * a.Hkv + kvh * nt;
+        add_pieces<D>(a, e, M, z, unit, share_owner<kFoldCtas>(s, total), share_owner<kFoldCtas>(s + nt - 1, total),
+                      (int)(blockIdx.x % parts), parts);
+        return;
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    move_rows<T, D>(k_pages, v_pages, weights, a, e, blockIdx.x - adders, blocks);
 }
 
 }  // namespace paged

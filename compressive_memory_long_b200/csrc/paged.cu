@@ -425,15 +425,13 @@ int launch_evict(T *kp, T *vp, float *weights, const PageArgs &a, const EvictArg
                                                  FoldTile<T, D>::SMEM, st, kp, vp, a, e, M));
             if (rc != INFINI_OK) return rc;
         }
-        TraceScope trace("evict_reduce", st);
-        const int rc = launched(launch_early(k_evict_reduce<D>, dim3((unsigned)units, (D * D / 4 + 255) / 256), 256, 0,
-                                             st, a, e, M, z));
-        if (rc != INFINI_OK) return rc;
     }
-    TraceScope trace("evict_move", st);
+    TraceScope trace("evict_finish", st);
     const int blocks = (e.budget + RowTile<T, D>::ROWS - 1) / RowTile<T, D>::ROWS;
-    return launched(launch_early(k_evict_move<T, D>, dim3((unsigned)(units * blocks)), 256, 0, st, kp, vp, weights, a,
-                                 e, blocks));
+    // adding blocks: some for every SM, at most one per 32 float4 columns, and one for z
+    const int parts = M && e.gone ? 1 + (int)std::max<int64_t>(1, std::min<int64_t>(D * D / 128, 1184 / units)) : 0;
+    return launched(launch_early(k_evict_finish<T, D>, dim3((unsigned)(units * (blocks + parts))), 256, 0, st, kp, vp,
+                                 weights, a, e, M, z, units, parts, blocks));
 }
 
 template <typename T>

@@ -33,16 +33,21 @@ __device__ __forceinline__ int cached_rows(const PageArgs &a, int64_t b)
     return (int)most;
 }
 
-// Row index of (b, kv head, r) within the pool, in rows of d elements; -1 for a bad page.
-__device__ __forceinline__ int64_t pool_row(const PageArgs &a, const int *table_row, int64_t r, int kvh)
+// Row index of (b, kv head, r) within the pool, in rows of d elements; -1 for a bad page, noted
+// in `bad`.  A caller with several rows reports once, after its loads: a store between them would
+// put the loads one after the other.
+__device__ __forceinline__ int64_t place_of(const PageArgs &a, const int *table_row, int64_t r, int kvh, bool &bad)
 {
     const int64_t i = r >> a.shift;
     const int pg = i < a.max_pages ? table_row[i] : -1;
-    if (pg < 0 || pg >= a.P) {
-        g_page_status = 1;
-        return -1;
-    }
-    return ((((int64_t)pg * a.Hkv + kvh) << a.shift) | (r & (((int64_t)1 << a.shift) - 1)));
+    const bool ok = pg >= 0 && pg < a.P;
+    bad |= !ok;
+    return ok ? ((((int64_t)pg * a.Hkv + kvh) << a.shift) | (r & (((int64_t)1 << a.shift) - 1))) : -1;
+}
+
+__device__ __forceinline__ void report(bool bad)
+{
+    if (bad) g_page_status = 1;
 }
 
 __device__ __forceinline__ uint32_t s_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -99,6 +104,7 @@ k_paged_append(const T *__restrict__ k, const T *__restrict__ v, T *k_pages, T *
     uint4 *kp = reinterpret_cast<uint4 *>(k_pages), *vp = reinterpret_cast<uint4 *>(v_pages);
     uint4 x[4], y[4];
     int64_t row[4];
+    bool bad = false;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
         const int64_t i = i0 + line + u * LINES;
@@ -108,9 +114,10 @@ k_paged_append(const T *__restrict__ k, const T *__restrict__ v, T *k_pages, T *
             const int kvh = (int)(i % a.Hkv);
             x[u] = load_chunk<T, ALIGNED>(k + b * sk0 + kvh * sk1 + t * sk2, c);
             y[u] = load_chunk<T, ALIGNED>(v + b * sv0 + kvh * sv1 + t * sv2, c);
-            row[u] = pool_row(a, a.table + b * a.max_pages, len + t, kvh);
+            row[u] = place_of(a, a.table + b * a.max_pages, len + t, kvh, bad);
         }
     }
+    report(bad);
 #pragma unroll
     for (int u = 0; u < 4; ++u)
         if (row[u] >= 0) {

@@ -617,11 +617,13 @@ k_paged_join(const T *__restrict__ q, float *weights, T *__restrict__ out, PageA
     float so_far[PER];
     auto load_weights = [&](int64_t j0) {
         const int *table = a.table + b * a.max_pages;
+        bool bad = false;
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
             const int64_t j = j0 + e * NT + tid;
-            place[e] = j < n ? pool_row(a, table, j, kvh) : -1;
+            place[e] = j < n ? place_of(a, table, j, kvh, bad) : -1;
         }
+        report(bad);
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
             const int64_t j = j0 + e * NT + tid;
