@@ -62,7 +62,17 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-__device__ __forceinline__ int2 peer_ld(const int *p, uint32_t rank)
+__device__ __forceinline__ int peer_ld(const int *p, uint32_t rank)
+{
+    uint32_t at;
+    int v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ int2 peer_ld2(const int *p, uint32_t rank)
 {
     uint32_t at;
     int2 v;
@@ -85,8 +95,8 @@ k_evict_select(const float *__restrict__ weights, PageArgs a, EvictArgs e, int C
     extern __shared__ int s_dyn[];
     int *hist = s_dyn;                                               // [3][kBins]
     uint32_t *keys = reinterpret_cast<uint32_t *>(s_dyn + 3 * kBins);   // [cap]
-    __shared__ int s_warp[NW], s_gt[NW], s_eq[NW];
-    __shared__ __align__(8) int s_tot[2];
+    __shared__ int s_gt[NW], s_eq[NW];
+    __shared__ __align__(8) int s_tot[2], groups[3 * 64];
     __shared__ int s_digit, s_rank;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t unit = blockIdx.x / CS, b = unit / a.Hkv;
@@ -134,37 +144,57 @@ k_evict_select(const float *__restrict__ weights, PageArgs a, EvictArgs e, int C
                 if (pass == 0 || (key >> (shift + bits)) == (thr >> (shift + bits)))
                     atomicAdd(&h[(key >> shift) & ((1 << bits) - 1)], 1);
             }
+            __syncthreads();
+            // a warp's 64 bins are two groups
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int sum = __reduce_add_sync(0xffffffffu, h[warp * 64 + k * 32 + lane]);
+                if (lane == 0) groups[pass * 64 + warp * 2 + k] = sum;
+            }
             if (CS > 1) cluster_sync();
             else __syncthreads();
-            // bins from the top, two per thread: thread tid has bins 2047 - 2 tid and the next
-            int x0 = 0, x1 = 0;
-            const int top = kBins - 1 - 2 * tid;
-            if (CS == 1) {
-                x0 = h[top];
-                x1 = h[top - 1];
-            } else {
+            // Warp 0 finds the digit: the bin where the count from the top reaches `left`.  First
+            // among 64 groups of 32 bins (each CTA's sums), two to a lane, then among a group's.
+            if (warp == 0) {
+                const int *gr = groups + pass * 64;
+                int x0 = 0, x1 = 0;
+                const int hi = 62 - 2 * lane;              // groups hi + 1 and hi, from the top
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
                     if (c < CS) {
-                        const int2 y = peer_ld(h + top - 1, c);
+                        const int2 y = CS > 1 ? peer_ld2(gr + hi, c) : *reinterpret_cast<const int2 *>(gr + hi);
                         x0 += y.y;
                         x1 += y.x;
                     }
-            }
-            int inc = x0 + x1;
+                int inc = x0 + x1;
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, inc, off);
-                if (lane >= off) inc += y;
-            }
-            if (lane == 31) s_warp[warp] = inc;
-            __syncthreads();
-            const int above = inc - x0 - x1 + before_warp(s_warp, warp, lane);
-            // the digit: the bin where the count from the top reaches `left`
-            if (above < left && left <= above + x0 + x1) {
-                const bool first = left <= above + x0;
-                s_digit = first ? top : top - 1;
-                s_rank = left - above - (first ? 0 : x0);
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, inc, off);
+                    if (lane >= off) inc += y;
+                }
+                int above = inc - x0 - x1;
+                bool here = above < left && left <= inc;
+                int g = left <= above + x0 ? hi + 1 : hi;
+                if (g == hi) above += x0;
+                const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+                g = __shfl_sync(0xffffffffu, g, src);
+                above = __shfl_sync(0xffffffffu, above, src);
+                int x = 0;
+                const int bin = g * 32 + 31 - lane;
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    if (c < CS) x += CS > 1 ? peer_ld(h + bin, c) : h[bin];
+                inc = x;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, inc, off);
+                    if (lane >= off) inc += y;
+                }
+                above += inc - x;
+                if (above < left && left <= above + x) {
+                    s_digit = bin;
+                    s_rank = left - above;
+                }
             }
             __syncthreads();
             thr |= (uint32_t)s_digit << shift;
@@ -196,7 +226,7 @@ k_evict_select(const float *__restrict__ weights, PageArgs a, EvictArgs e, int C
 #pragma unroll
     for (int c = 0; c < 7; ++c)
         if (c < rank) {
-            const int2 y = peer_ld(s_tot, c);
+            const int2 y = peer_ld2(s_tot, c);
             gt += y.x;
             eq += y.y;
         }
@@ -261,17 +291,15 @@ struct FoldTile {
     static constexpr uint32_t COLS = 4 * D;                // two buffers of two accumulators
 };
 
-// sigma of two values, as max(x, 0) + e^min(x, 0) (a NaN passes through the maximum).
+// sigma of two values, as max(x, 0) + min(e^x, 1): the saturating addition is the minimum, and off
+// the pipe that the parts' conversions fill.  A NaN passes through the maximum.
 __device__ __forceinline__ uint64_t sigma2(float x, float y)
 {
-    float p, q;
+    float p, q, e0, e1;
     asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(p) : "f"(x));
     asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(q) : "f"(y));
-    const uint64_t e = tc::f2_mul(tc::f2_pack(fminf(x, 0.f), fminf(y, 0.f)),
-                                  tc::f2_pack(1.4426950408889634f, 1.4426950408889634f));
-    float e0, e1;
-    tc::f2_unpack(e, e0, e1);
-    return tc::f2_add(tc::f2_pack(p, q), tc::f2_pack(tc::ex2(e0), tc::ex2(e1)));
+    tc::f2_unpack(tc::f2_mul(tc::f2_pack(x, y), tc::f2_pack(1.4426950408889634f, 1.4426950408889634f)), e0, e1);
+    return tc::f2_add(tc::f2_pack(p, q), tc::f2_pack(__saturatef(tc::ex2(e0)), __saturatef(tc::ex2(e1))));
 }
 
 // x = h + m + l in bf16 parts, to 2^-25 of it; pairs packed.
