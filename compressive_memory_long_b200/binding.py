@@ -345,6 +345,7 @@ def backward(q, k, v, beta, M0, z0, dout, dM=None, dz=None, *, N: int, rule="lin
 
 # ---- serving from a paged cache ------------------------------------------------------------
 
+_Tensor = torch.Tensor
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _FN = {(name, dt): getattr(LIB, name + tail)
        for name in ("infini_attn_rotary", "infini_attn_rotary_bwd", "infini_attn_paged_append",
@@ -385,9 +386,10 @@ def _at(t, name, dtype, shape, device):
     """The address of a contiguous tensor of this type and shape (None stays None)."""
     if t is None:
         return None
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.device == device and t.is_contiguous()):
-        _check(t, name, dtype, shape, device)
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.get_device() == device.index and t.is_cuda):
+        return t.data_ptr()
+    _check(t, name, dtype, shape, device)
     return t.data_ptr()
 
 
@@ -404,15 +406,15 @@ def _evict_bytes(*sizes):
 def _strides(t, name, dtype, shape, device):
     """Element strides (batch, head, token) of a [B, H, L, d] view with contiguous rows; None
     for a contiguous one."""
-    if not isinstance(t, torch.Tensor) or t.device != device:
+    if not isinstance(t, _Tensor) or t.get_device() != device.index or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.dtype != dtype or t.shape != shape or t.stride(3) != 1:
+    s = t.stride()
+    if t.dtype is not dtype or t.shape != shape or s[3] != 1:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)} with contiguous rows, got "
-                         f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}")
+                         f"{t.dtype} {tuple(t.shape)}, strides {s}")
     if t.is_contiguous():
         return None
     B, H, L, d = shape
-    s = t.stride()
     # a dimension of one entry may carry any stride: name the contiguous one
     return (_I64 * 3)(s[0] if B > 1 else H * L * d, s[1] if H > 1 else L * d, s[2] if L > 1 else d)
 
@@ -424,12 +426,12 @@ def _rotary_call(handle, dev, name, q, k, freq, positions, start, interleaved, s
     sq = _strides(q, "q", dt, shape, dev)
     Hkv, kp, sk = 0, None, None
     if q_out is None:
-        q_out = torch.empty(shape, dtype=dt, device=dev)
+        q_out = q.new_empty(shape)
     if k is not None:
         Hkv, kp, kshape = k.shape[1], k.data_ptr(), (B, k.shape[1], L, d)
         sk = _strides(k, "k", dt, kshape, dev)
         if k_out is None:
-            k_out = torch.empty(kshape, dtype=dt, device=dev)
+            k_out = k.new_empty(kshape)
     elif k_out is not None:
         raise ValueError("k_out without k")
     half = freq.numel()
@@ -515,18 +517,18 @@ def _decode_call(handle, dev, q, k, v, k_pages, v_pages, page_table, lens, beta,
     H, dt, f32 = q.shape[1], k_pages.dtype, torch.float32
     shape, kshape = (B, H, d), (B, Hkv, d)
     fn = _entry("infini_attn_paged_decode_step", dt)
-    qp = _at(q, "q", dt, shape, dev)
+    qp, lp = _at(q, "q", dt, shape, dev), _at(lens, "lens", torch.int32, (B,), dev)
     rot = 0
     if freq is not None:
         rot = 2 * freq.numel()
     elif positions is not None:
         raise ValueError("positions without freq")
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=dev)
+        out = q.new_empty(shape)
     need = _decode_bytes(B, H, Hkv, d, P, page, 0 if weights is None else 1)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    ws = lens.new_empty((need + 3) // 4) if need else None
     _run(fn, qp, _at(k, "k", dt, kshape, dev), _at(v, "v", dt, kshape, dev), kp, vp, tp,
-         _at(lens, "lens", torch.int32, (B,), dev), _at(beta, "beta", f32, (H,), dev),
+         lp, _at(beta, "beta", f32, (H,), dev),
          _at(M, "M", f32, (B, Hkv, d, d), dev), _at(z, "z", f32, kshape, dev), wp,
          _at(freq, "freq", torch.float64, (rot // 2,), dev),
          _at(positions, "positions", torch.int64, (B,), dev), _at(out, "out", dt, shape, dev),
@@ -563,15 +565,16 @@ def _evict_call(handle, dev, k_pages, v_pages, weights, page_table, lens, dst_ta
     if Bd != B:
         raise ValueError(f"dst_table has {Bd} rows, page_table {B}")
     i32, f32 = torch.int32, torch.float32
+    lp = _at(lens, "lens", i32, (B,), dev)
     if lens_out is None:
-        lens_out = torch.empty((B,), dtype=i32, device=dev)
+        lens_out = lens.new_empty((B,))
     shape = (B, Hkv, max(budget, 0))
     if kept is None:
-        kept = torch.empty(shape, dtype=i32, device=dev)
+        kept = lens.new_empty(shape)
     need = _evict_bytes(B, Hkv, d, page, max_pages, budget, 0 if M is None else 1)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _run(_entry("infini_attn_paged_evict", k_pages.dtype), kp, vp, wp, tp,
-         _at(lens, "lens", i32, (B,), dev), dp, _at(lens_out, "lens_out", i32, (B,), dev),
+    ws = lens.new_empty((need + 3) // 4) if need else None
+    _run(_entry("infini_attn_paged_evict", k_pages.dtype), kp, vp, wp, tp, lp, dp,
+         _at(lens_out, "lens_out", i32, (B,), dev),
          _at(kept, "kept", i32, shape, dev), _at(M, "M", f32, (B, Hkv, d, d), dev),
          _at(z, "z", f32, (B, Hkv, d), dev), None if ws is None else ws.data_ptr(), need, B, Hkv, d, P,
          page, max_pages, dst_pages, budget, recent, RULES[rule], handle)
