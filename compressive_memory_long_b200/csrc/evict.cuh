@@ -267,6 +267,8 @@ k_evict_select(const float *__restrict__ weights, PageArgs a, EvictArgs e, int C
 // tensor rate at that speed.
 constexpr int kFoldCtas = 148;
 constexpr int kFoldLoaders = 16, kFoldReaders = 8;
+// 28 warps, launched with 72 registers a thread (64512 in all); the loaders go down to 64 and the
+// issuing warpgroup to 24, which gives the readers their 104.
 constexpr int kFoldThreads = 32 * (kFoldLoaders + kFoldReaders + 4);
 constexpr int kFoldRows = 256;       // rows of a tile: one reading of the accumulators
 
@@ -321,7 +323,7 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
     using Tile = FoldTile<T, D>;
     constexpr int CPR = Tile::CPR, LD = Tile::LD, E = Tile::E, SUB = Tile::SUB, HALF = Tile::HALF, VP = Tile::VP, ST = 2;
     extern __shared__ unsigned char s_raw[];
-    __shared__ __align__(8) uint64_t full[ST], empty[ST], tfull[2], tempty[2];
+    __shared__ __align__(8) uint64_t full[ST], empty[ST], tfull[2], tempty[2], drained;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     __shared__ ShareScratch s_share;
@@ -347,6 +349,7 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
             tc::mbar_init(&tfull[i], 1);
             tc::mbar_init(&tempty[i], kFoldReaders);
         }
+        tc::mbar_init(&drained, 1);
         s_abort = 0;
         tc::fence_barrier_init();
     }
@@ -627,9 +630,11 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
             }
             tc::mma_commit(&tfull[buf]);
         }
-        // the last products end before TMEM is given back
-        for (int64_t s = steps > 2 ? steps - 2 : 0; s < steps; ++s)
-            tc::mbar_wait(&tfull[s & 1], (uint32_t)((s >> 1) & 1), abort, 94);
+        // every product issued ends before TMEM is given back, whatever gave up before
+        tc::mma_commit(&drained);
+        const long long t_end = clock64();
+        while (!tc::mbar_try_wait(&drained, 0) && clock64() - t_end < tc::kSpinLimitCycles) {
+        }
       }
     }
     __syncwarp();

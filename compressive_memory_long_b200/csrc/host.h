@@ -22,4 +22,7 @@ private:
 // up, and page numbers or rows outside a cache.  INFINI_OK, or INFINI_ERR_CUDA if a copy failed.
 int take_paged_status(bool &waits, bool &pages);
 
+// The bound of the paged entries' device waits, in SM cycles.
+int set_paged_wait_limit(long long cycles);
+
 }  // namespace infini

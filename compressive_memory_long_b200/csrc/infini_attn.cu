@@ -1524,7 +1524,7 @@ int infini_attn_test_wait_limit(int64_t cycles)
 {
     const long long v = cycles > 0 ? (long long)cycles : infini::tc::kSpinLimitCycles;
     return cudaMemcpyToSymbol(infini::tc::g_spin_limit, &v, sizeof(v)) == cudaSuccess
-        ? INFINI_OK : INFINI_ERR_CUDA;
+        ? infini::set_paged_wait_limit(v) : INFINI_ERR_CUDA;
 }
 
 int infini_attn_test_withhold_publish(int on)

@@ -32,6 +32,11 @@ int take_paged_status(bool &waits, bool &pages)
     return INFINI_OK;
 }
 
+int set_paged_wait_limit(long long cycles)
+{
+    return cudaMemcpyToSymbol(tc::g_spin_limit, &cycles, sizeof(cycles)) == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
+}
+
 namespace {
 
 using namespace paged;
