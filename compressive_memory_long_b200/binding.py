@@ -17,7 +17,6 @@ the entry point from the activation dtype.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 import torch
@@ -344,102 +343,25 @@ def backward(q, k, v, beta, M0, z0, dout, dM=None, dz=None, *, N: int, rule="lin
 
 
 # ---- serving from a paged cache ------------------------------------------------------------
+# Checks, allocations and the C calls are native (csrc/py_paged.cpp): these steps take a few
+# microseconds on the GPU, less than the same checks in Python.
 
-_Tensor = torch.Tensor
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_FN = {(name, dt): getattr(LIB, name + tail)
-       for name in ("infini_attn_rotary", "infini_attn_rotary_bwd", "infini_attn_paged_append",
-                    "infini_attn_paged_decode_step", "infini_attn_paged_evict")
-       for dt, tail in ((torch.bfloat16, ""), (torch.float32, "_f32"))}
+if not os.path.exists(_build.EXT) and os.environ.get("INFINI_NO_AUTOBUILD") != "1":
+    _build.build_ext()
+from . import _paged  # noqa: E402
 
-
-def _launch(device, stream, body, *args):
-    """body(stream handle, device, *args) with the device and stream of the call current:
-    allocations inside belong to the stream it runs on."""
-    if not isinstance(device, torch.device) or device.type != "cuda":
-        raise ValueError("the tensors must be on a CUDA device")
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-        with torch.cuda.stream(stream):       # sets the device too
-            return body(stream.cuda_stream, device, *args)
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return body(_raw_stream(device.index), device, *args)
-    return body(_raw_stream(device.index), device, *args)
+_paged.set_error(InfiniError)
 
 
-def _entry(name, dtype):
-    fn = _FN.get((name, dtype))
-    if fn is None:
-        raise ValueError(f"unsupported activation dtype {dtype}")
-    return fn
-
-
-def _run(fn, *args):
-    rc = fn(*args)
-    if rc != 0:
-        raise InfiniError(rc, infini_attn_status_string(rc))
-
-
-def _at(t, name, dtype, shape, device):
-    """The address of a contiguous tensor of this type and shape (None stays None)."""
-    if t is None:
-        return None
-    if (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
-            and t.get_device() == device.index and t.is_cuda):
-        return t.data_ptr()
-    _check(t, name, dtype, shape, device)
-    return t.data_ptr()
-
-
-@functools.lru_cache(maxsize=256)
-def _decode_bytes(*sizes):
-    return LIB.infini_attn_paged_decode_workspace_bytes(*sizes)
-
-
-@functools.lru_cache(maxsize=256)
-def _evict_bytes(*sizes):
-    return LIB.infini_attn_paged_evict_workspace_bytes(*sizes)
-
-
-def _strides(t, name, dtype, shape, device):
-    """Element strides (batch, head, token) of a [B, H, L, d] view with contiguous rows; None
-    for a contiguous one."""
-    if not isinstance(t, _Tensor) or t.get_device() != device.index or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    s = t.stride()
-    if t.dtype is not dtype or t.shape != shape or s[3] != 1:
-        raise ValueError(f"{name}: expected {dtype} {tuple(shape)} with contiguous rows, got "
-                         f"{t.dtype} {tuple(t.shape)}, strides {s}")
-    if t.is_contiguous():
-        return None
-    B, H, L, d = shape
-    # a dimension of one entry may carry any stride: name the contiguous one
-    return (_I64 * 3)(s[0] if B > 1 else H * L * d, s[1] if H > 1 else L * d, s[2] if L > 1 else d)
-
-
-def _rotary_call(handle, dev, name, q, k, freq, positions, start, interleaved, scale, q_out, k_out):
-    dt, shape = q.dtype, q.shape
-    fn = _entry(name, dt)
-    B, H, L, d = shape
-    sq = _strides(q, "q", dt, shape, dev)
-    Hkv, kp, sk = 0, None, None
-    if q_out is None:
-        q_out = q.new_empty(shape)
-    if k is not None:
-        Hkv, kp, kshape = k.shape[1], k.data_ptr(), (B, k.shape[1], L, d)
-        sk = _strides(k, "k", dt, kshape, dev)
-        if k_out is None:
-            k_out = k.new_empty(kshape)
-    elif k_out is not None:
-        raise ValueError("k_out without k")
-    half = freq.numel()
-    _run(fn, q.data_ptr(), kp, _at(q_out, "q_out", dt, shape, dev),
-         _at(k_out, "k_out", dt, (B, Hkv, L, d), dev), _at(freq, "freq", torch.float64, (half,), dev),
-         _at(positions, "positions", torch.int64, (B, L), dev), int(start), sq, sk, B, H, Hkv, L, d,
-         2 * half, 1 if interleaved else 0, float(scale), handle)
-    return q_out, k_out
+def _on(stream, t, call, *args):
+    """call(*args) with ``stream`` current (None: the current one), so that what it allocates
+    belongs to the stream it runs on."""
+    if stream is None:
+        return call(*args)
+    if stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    with torch.cuda.stream(stream):
+        return call(*args)
 
 
 def rotary(q, k, freq, *, positions=None, start: int = 0, interleaved: bool = False, scale=1.0,
@@ -453,49 +375,14 @@ def rotary(q, k, freq, *, positions=None, start: int = 0, interleaved: bool = Fa
     positions [B,L] int64, or None: token t is at ``start + t``.  ``scale`` multiplies the
     turned channels.  q_out / k_out may be their own contiguous inputs.  Returns (q_out, k_out).
     """
-    if q.dim() != 4 or (k is not None and k.dim() != 4):
-        raise ValueError("q and k are [B, H, L, d] and [B, Hkv, L, d]")
-    return _launch(q.device, stream, _rotary_call, "infini_attn_rotary", q, k, freq, positions, start,
-                   interleaved, scale, q_out, k_out)
+    return _on(stream, q, _paged.rotary, 0, q, k, freq, positions, start, interleaved, scale, q_out, k_out)
 
 
 def rotary_backward(dq_out, dk_out, freq, *, positions=None, start: int = 0,
                     interleaved: bool = False, scale=1.0, dq=None, dk=None, stream=None):
     """Gradients of ``rotary``'s inputs from those of its outputs (arguments as there)."""
-    if dq_out.dim() != 4 or (dk_out is not None and dk_out.dim() != 4):
-        raise ValueError("dq_out and dk_out are [B, H, L, d] and [B, Hkv, L, d]")
-    return _launch(dq_out.device, stream, _rotary_call, "infini_attn_rotary_bwd", dq_out, dk_out, freq,
-                   positions, start, interleaved, scale, dq, dk)
-
-
-def _pool(k_pages, v_pages, weights, dev):
-    """Addresses of the pool's tensors and its shape."""
-    shape = k_pages.shape
-    if len(shape) != 4:
-        raise ValueError("k_pages and v_pages are [P, Hkv, page, d]")
-    dt = k_pages.dtype
-    return (_at(k_pages, "k_pages", dt, shape, dev), _at(v_pages, "v_pages", dt, shape, dev),
-            _at(weights, "weights", torch.float32, shape[:3], dev), shape)
-
-
-def _table(page_table, dev, name="page_table"):
-    if page_table.dim() != 2:
-        raise ValueError(f"{name} is [B, pages]")
-    shape = page_table.shape
-    return _at(page_table, name, torch.int32, shape, dev), shape[0], shape[1]
-
-
-def _append_call(handle, dev, k, v, k_pages, v_pages, page_table, lens, counts, weights):
-    kp, vp, wp, (P, Hkv, page, d) = _pool(k_pages, v_pages, weights, dev)
-    tp, B, max_pages = _table(page_table, dev)
-    if k.dim() != 4:
-        raise ValueError("k and v are [B, Hkv, T, d]")
-    dt, T = k_pages.dtype, k.shape[2]
-    shape = (B, Hkv, T, d)
-    sk, sv = _strides(k, "k", dt, shape, dev), _strides(v, "v", dt, shape, dev)
-    _run(_entry("infini_attn_paged_append", dt), k.data_ptr(), v.data_ptr(), sk, sv, kp, vp, wp, tp,
-         _at(lens, "lens", torch.int32, (B,), dev), _at(counts, "counts", torch.int32, (B,), dev), B,
-         Hkv, T, d, P, page, max_pages, handle)
+    return _on(stream, dq_out, _paged.rotary, 1, dq_out, dk_out, freq, positions, start, interleaved, scale,
+               dq, dk)
 
 
 def paged_append(k, v, k_pages, v_pages, page_table, lens, *, counts=None, weights=None,
@@ -506,35 +393,7 @@ def paged_append(k, v, k_pages, v_pages, page_table, lens, *, counts=None, weigh
     k_pages/v_pages [P,Hkv,page,d] (bf16 or fp32), page_table [B,max_pages] and lens [B] int32,
     weights [P,Hkv,page] fp32 or None.  lens is left to the caller.
     """
-    return _launch(k_pages.device, stream, _append_call, k, v, k_pages, v_pages, page_table, lens,
-                   counts, weights)
-
-
-def _decode_call(handle, dev, q, k, v, k_pages, v_pages, page_table, lens, beta, M, z, weights, freq,
-                 positions, interleaved, scale, out):
-    kp, vp, wp, (P, Hkv, page, d) = _pool(k_pages, v_pages, weights, dev)
-    tp, B, max_pages = _table(page_table, dev)
-    H, dt, f32 = q.shape[1], k_pages.dtype, torch.float32
-    shape, kshape = (B, H, d), (B, Hkv, d)
-    fn = _entry("infini_attn_paged_decode_step", dt)
-    qp, lp = _at(q, "q", dt, shape, dev), _at(lens, "lens", torch.int32, (B,), dev)
-    rot = 0
-    if freq is not None:
-        rot = 2 * freq.numel()
-    elif positions is not None:
-        raise ValueError("positions without freq")
-    if out is None:
-        out = q.new_empty(shape)
-    need = _decode_bytes(B, H, Hkv, d, P, page, 0 if weights is None else 1)
-    ws = lens.new_empty((need + 3) // 4) if need else None
-    _run(fn, qp, _at(k, "k", dt, kshape, dev), _at(v, "v", dt, kshape, dev), kp, vp, tp,
-         lp, _at(beta, "beta", f32, (H,), dev),
-         _at(M, "M", f32, (B, Hkv, d, d), dev), _at(z, "z", f32, kshape, dev), wp,
-         _at(freq, "freq", torch.float64, (rot // 2,), dev),
-         _at(positions, "positions", torch.int64, (B,), dev), _at(out, "out", dt, shape, dev),
-         None if ws is None else ws.data_ptr(), need, B, H, Hkv, d, P, page, max_pages, rot,
-         1 if interleaved else 0, float(scale), handle)
-    return out
+    return _on(stream, k_pages, _paged.append, k, v, k_pages, v_pages, page_table, lens, counts, weights)
 
 
 def paged_decode_step(q, k, v, k_pages, v_pages, page_table, lens, *, beta=None, M=None, z=None,
@@ -549,36 +408,8 @@ def paged_decode_step(q, k, v, k_pages, v_pages, page_table, lens, *, beta=None,
     read and gated in as in the forward.  With weights, every row's softmax weight is added to
     it.  lens < 0 marks a padding entry: its output is 0.  Returns out [B,H,d].
     """
-    if q.dim() != 3:
-        raise ValueError("q is [B, H, d]")
-    return _launch(q.device, stream, _decode_call, q, k, v, k_pages, v_pages, page_table, lens, beta,
-                   M, z, weights, freq, positions, interleaved, scale, out)
-
-
-def _evict_call(handle, dev, k_pages, v_pages, weights, page_table, lens, dst_table, budget, recent, M,
-                z, rule, lens_out, kept):
-    if weights is None:
-        raise ValueError("eviction needs the accumulated weights")
-    kp, vp, wp, (P, Hkv, page, d) = _pool(k_pages, v_pages, weights, dev)
-    tp, B, max_pages = _table(page_table, dev)
-    dp, Bd, dst_pages = _table(dst_table, dev, "dst_table")
-    if Bd != B:
-        raise ValueError(f"dst_table has {Bd} rows, page_table {B}")
-    i32, f32 = torch.int32, torch.float32
-    lp = _at(lens, "lens", i32, (B,), dev)
-    if lens_out is None:
-        lens_out = lens.new_empty((B,))
-    shape = (B, Hkv, max(budget, 0))
-    if kept is None:
-        kept = lens.new_empty(shape)
-    need = _evict_bytes(B, Hkv, d, page, max_pages, budget, 0 if M is None else 1)
-    ws = lens.new_empty((need + 3) // 4) if need else None
-    _run(_entry("infini_attn_paged_evict", k_pages.dtype), kp, vp, wp, tp, lp, dp,
-         _at(lens_out, "lens_out", i32, (B,), dev),
-         _at(kept, "kept", i32, shape, dev), _at(M, "M", f32, (B, Hkv, d, d), dev),
-         _at(z, "z", f32, (B, Hkv, d), dev), None if ws is None else ws.data_ptr(), need, B, Hkv, d, P,
-         page, max_pages, dst_pages, budget, recent, RULES[rule], handle)
-    return lens_out, kept
+    return _on(stream, q, _paged.decode, q, k, v, k_pages, v_pages, page_table, lens, beta, M, z, weights,
+               freq, positions, interleaved, scale, out)
 
 
 def paged_evict(k_pages, v_pages, weights, page_table, lens, dst_table, *, budget: int,
@@ -590,5 +421,5 @@ def paged_evict(k_pages, v_pages, weights, page_table, lens, dst_table, *, budge
     pages of their own.  With M [B,Hkv,d,d] and z [B,Hkv,d] the evicted rows are folded into the
     memory in place.  Returns (lens_out [B], kept [B,Hkv,budget] int32: old rows, -1 padded).
     """
-    return _launch(k_pages.device, stream, _evict_call, k_pages, v_pages, weights, page_table, lens,
-                   dst_table, int(budget), int(recent), M, z, rule, lens_out, kept)
+    return _on(stream, k_pages, _paged.evict, k_pages, v_pages, weights, page_table, lens, dst_table, budget,
+               recent, M, z, RULES[rule], lens_out, kept)
