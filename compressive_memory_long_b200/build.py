@@ -59,7 +59,9 @@ def build_ext(force: bool = False, verbose: bool = False) -> str:
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     dirs = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(cuda, "include"), *ce.include_paths()]
     tmp = EXT + f".tmp{os.getpid()}"
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+    # the system's g++, whose libstdc++ is the shared one torch uses: a compiler that links its own
+    # copy would throw exceptions that the other copy's handlers cannot take
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *[x for d in dirs for x in ("-isystem" if d != INCLUDE else "-I", d)], EXT_SRC, "-o", tmp,
            "-L", PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
