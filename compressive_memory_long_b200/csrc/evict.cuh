@@ -13,7 +13,7 @@
 
 #include "paged.cuh"
 #include "share.cuh"
-#include "tc_common.cuh"
+#include "tc_paged.cuh"
 
 namespace infini {
 namespace paged {
@@ -253,18 +253,23 @@ k_evict_select(const float *__restrict__ weights, PageArgs a, EvictArgs e, int C
 // ---- fold ---------------------------------------------------------------------------------------
 //
 // sum sigma(k) v^T over a head's evicted rows, on tcgen05: A = sigma(K)^T (M = the key features),
-// B = V (N = the value features), both staged row by row (MN-major), 64 rows a stage.  M and z are
-// 32-bit sums, so sigma(k) is split into three bf16 parts (24 bits; two would leave 2^-18, more
-// than the sum's own rounding), v into one (bf16, exact) or three (fp32: the six products down to
-// 2^-24 are kept).  The leading product has an accumulator of its own and every 256 rows' result is
-// read out and added in registers: the tensor core's own additions over a long axis lose about
-// one unit per addition, all in one direction.
+// B = V (N = the value features), both staged row by row (MN-major), 64 rows a stage (fp32: 32).
+// M and z are 32-bit sums, so sigma(k) is split into three bf16 parts (24 bits; two would leave
+// 2^-17 of it, more than the sum's own rounding), v into one (bf16, exact) or three (fp32: the six
+// products down to 2^-24 are kept).  The tensor core's additions over a long axis lose about one
+// unit each, all in one direction: the leading product and the others have accumulators of their
+// own, and both are read out and added in registers every 256 rows (twice as many additions
+// between two readings raised the error of a 63,000-row sum from 2e-7 to 7e-7).
 //
 // The evicted rows of all heads are shared out evenly over 148 CTAs (share.cuh).  In each, 16
 // loader warps copy rows two stages ahead (64 KB in flight), form sigma and the parts and sum z;
-// one thread issues the products; eight warps read the accumulators.  Reading K and V is the
-// bound (4 d bytes a row against 2 d^2 operations); the parts' products are a quarter of the
-// tensor rate at that speed.
+// one thread issues the products; eight warps read the accumulators.  Reading K and V is the floor
+// (4 d bytes a row against 2 d^2 operations), 1400 cycles for a stage (bf16, d = 128).  Shared
+// memory is the bound: copies and parts move 96 KB through it and the products' operands 96 KB,
+// 1500 cycles at 128 bytes, and a stage takes 2200 (65500 rows of 8 heads: 80 us, 3.3 TB/s).
+// Tried without gain: sigma as max(k, 0) + e^min(k, 0) with the first term taken as a part (fewer
+// instructions, the same time); z as a product with a column of ones (reads sigma's parts once
+// more: 98 us).
 constexpr int kFoldCtas = 148;
 constexpr int kFoldLoaders = 16, kFoldReaders = 8;
 // 28 warps, launched with 72 registers a thread (64512 in all); the loaders go down to 64 and the

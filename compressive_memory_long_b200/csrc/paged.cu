@@ -21,10 +21,10 @@ int take_paged_status(bool &waits, bool &pages)
 {
     int v[2] = {0, 0};
     const int zero = 0;
-    if (cudaMemcpyFromSymbol(&v[0], tc::g_wait_status, sizeof(int)) != cudaSuccess ||
+    if (cudaMemcpyFromSymbol(&v[0], tc::g_paged_wait_status, sizeof(int)) != cudaSuccess ||
         cudaMemcpyFromSymbol(&v[1], paged::g_page_status, sizeof(int)) != cudaSuccess)
         return INFINI_ERR_CUDA;
-    if ((v[0] != 0 && cudaMemcpyToSymbol(tc::g_wait_status, &zero, sizeof(int)) != cudaSuccess) ||
+    if ((v[0] != 0 && cudaMemcpyToSymbol(tc::g_paged_wait_status, &zero, sizeof(int)) != cudaSuccess) ||
         (v[1] != 0 && cudaMemcpyToSymbol(paged::g_page_status, &zero, sizeof(int)) != cudaSuccess))
         return INFINI_ERR_CUDA;
     waits = v[0] != 0;
@@ -34,7 +34,7 @@ int take_paged_status(bool &waits, bool &pages)
 
 int set_paged_wait_limit(long long cycles)
 {
-    return cudaMemcpyToSymbol(tc::g_spin_limit, &cycles, sizeof(cycles)) == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
+    return cudaMemcpyToSymbol(tc::g_paged_spin_limit, &cycles, sizeof(cycles)) == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
 }
 
 namespace {

@@ -23,23 +23,23 @@
 namespace infini {
 namespace tc {
 
-// Device-side status word shared by every kernel of a translation unit that waits on a
-// barrier (each unit has its own; infini_attn_device_status reads all): 0 = fine, otherwise the id of the first wait that gave up.
-static __device__ int g_wait_status;
+// Device-side status word shared by every kernel of this library that waits on a
+// barrier: 0 = fine, otherwise the id of the first wait that gave up.
+__device__ int g_wait_status;
 
 // About 0.5 s at the B200's top SM clock: far above any legitimate wait in these kernels.
 constexpr long long kSpinLimitCycles = 1000000000LL;
 
 // The bound every wait applies, in SM clock cycles.  Only a test hook lowers it
 // (infini_attn_test_wait_limit), to make a withheld publish time out quickly.
-static __device__ long long g_spin_limit = kSpinLimitCycles;
+__device__ long long g_spin_limit = kSpinLimitCycles;
 
 __device__ __forceinline__ long long spin_limit() { return g_spin_limit; }
 
 // Test hook (infini_attn_test_withhold_publish): when nonzero, the first unit of every head
 // in the fused 64-token kernel publishes nothing, so the bounded waits of the units after it
 // run out and report INFINI_ERR_TIMEOUT.
-static __device__ int g_test_withhold;
+__device__ int g_test_withhold;
 
 // The status word is sticky: once a wait anywhere has given up, every other CTA stops
 // waiting and later launches return at once, until the host reads and clears it.
