@@ -231,7 +231,8 @@ int paged_append(const void *k, const void *v, const int64_t *k_strides, const i
     PageArgs a{table, lens, P, (int)max_pages, 0, (int)Hkv};
     const int rc = check_pool(B, Hkv, P, page, max_pages, &a.shift);
     if (rc == INFINI_ERR_INVALID_ARG) return rc;
-    if (Tn > ((int64_t)1 << 30) || B * Hkv * Tn > ((int64_t)1 << 32)) return INFINI_ERR_INVALID_ARG;
+    if (Tn > ((int64_t)1 << 30) || Hkv * Tn > ((int64_t)1 << 30) || B * Hkv * Tn > ((int64_t)1 << 32))
+        return INFINI_ERR_INVALID_ARG;
     const int64_t es = (int64_t)sizeof(T), pool = P * Hkv * page;
     int64_t sk[3], sv[3];
     if (!take_strides(k_strides, Hkv, Tn, d, sk) || !take_strides(v_strides, Hkv, Tn, d, sv))
@@ -256,7 +257,8 @@ int paged_append(const void *k, const void *v, const int64_t *k_strides, const i
         const int64_t blocks = (Tn * Hkv + RowTile<T, D>::ROWS - 1) / RowTile<T, D>::ROWS;          \
         if (B * blocks > ((int64_t)1 << 31) - 1) return INFINI_ERR_INVALID_ARG;                     \
         k_paged_append<T, D, ALIGNED><<<(unsigned)(B * blocks), 256, 0, st>>>(                      \
-            tk, tv, kp, vp, weights, a, counts, sk[0], sk[1], sk[2], sv[0], sv[1], sv[2], Tn, blocks); \
+            tk, tv, kp, vp, weights, a, counts, sk[0], sk[1], sk[2], sv[0], sv[1], sv[2], (int)Tn, \
+            (uint32_t)blocks);                                                                      \
     } while (0)
     switch (d) {
     case 32: if (rows) APPEND(32, true); else APPEND(32, false); break;

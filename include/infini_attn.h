@@ -257,7 +257,8 @@ INFINI_API int infini_attn_rotary_bwd_f32(const void *dq_out, const void *dk_out
  *
  * infini_attn_paged_append: rows lens[b] .. lens[b] + counts[b] - 1 become the first counts[b]
  * tokens of k, v [B, Hkv, T, d] (strides as for infini_attn_rotary; counts [B] int32, NULL: T
- * for every sequence; a count beyond T counts as T), and their weights 0.
+ * for every sequence; a count beyond T counts as T), and their weights 0.  T * Hkv may not
+ * exceed 2^30.
  */
 INFINI_API int infini_attn_paged_append(const void *k, const void *v, const int64_t *k_strides,
                                         const int64_t *v_strides, void *k_pages, void *v_pages,
@@ -287,7 +288,12 @@ INFINI_API int infini_attn_paged_append_f32(const void *k, const void *v, const 
  *     The pages of a sequence must then be its own.
  * Padding entries (lens < 0) give rows of 0.
  *   q [B, H, d], k / v [B, Hkv, d], out [B, H, d];  out and the workspace overlap nothing.
- *   workspace: infini_attn_paged_decode_workspace_bytes(B, H, Hkv, d, P, page, weights != NULL)
+ *   workspace: infini_attn_paged_decode_workspace_bytes(B, H, Hkv, d, P, page, weights != NULL):
+ *     about (296 + B * Hkv) * (d + 2) * 4 bytes per query head of a group, and with weights
+ *     P * page * H * 4 more (every cached row's scores)
+ * The rows of all sequences are shared out over the SMs by the device, whatever the lengths; up
+ * to eight query heads of a group share one reading of its rows, larger groups read them again.
+ * Results do not depend on the run: nothing is summed in an order that may change.
  */
 INFINI_API int infini_attn_paged_decode_step(
     const void *q, const void *k, const void *v, void *k_pages, void *v_pages,
@@ -321,7 +327,10 @@ INFINI_API int64_t infini_attn_paged_decode_workspace_bytes(int64_t B, int64_t H
  *   M, z (both or none): the rows not kept are folded in, in place, as one update of the
  *     forward's rule.  INFINI_UPDATE_DELTA is not built: INFINI_ERR_UNSUPPORTED.
  *   workspace: infini_attn_paged_evict_workspace_bytes(B, Hkv, d, page, max_pages, budget,
- *     M != NULL)
+ *     M != NULL): nothing without a memory; else 4 bytes for every row of the table beyond the
+ *     budget and key/value head, and about (148 + B * Hkv) * d * d * 4
+ * A wait of the fold's that gives up is reported as INFINI_ERR_TIMEOUT by
+ * infini_attn_device_status.  budget may not exceed 2^30.
  */
 INFINI_API int infini_attn_paged_evict(void *k_pages, void *v_pages, float *weights,
                                        const int32_t *page_table, const int32_t *lens,
