@@ -97,7 +97,9 @@ struct Vec {
     }
 };
 
-// Bandwidth is the bound: every element is read and written once.  A thread owns two 16-byte
+// Bandwidth is the bound: every element is read and written once (40 heads of 32768 tokens, d = 128,
+// bf16, read token by token: 671 MB in 108 us, 6.2 TB/s; fp32 gradients at positions near a million
+// 537 MB in 85 us, 6.3 TB/s; one element at a time took 260 and 131 us).  A thread owns two 16-byte
 // vectors of a token's row and applies its turns, formed once, to its heads, four heads' loads
 // in flight at a time.  The vectors are
 //   kHalves:  channels c and c + rot/2 (rot/2 a whole number of vectors), or two copied ones;
