@@ -126,13 +126,13 @@ bool row_aligned(const void *p, const int64_t s[3], int64_t es)
 }
 
 template <typename T, int D>
-int launch_rotary(const T *q, const T *k, T *q_out, T *k_out, const RotaryArgs &a, int64_t B, bool rows, bool apart,
+int launch_rotary(const T *q, const T *k, T *q_out, T *k_out, const RotaryArgs &a, int64_t B, bool rows,
                   cudaStream_t st)
 {
     TraceScope trace("rotary", st);
     constexpr int N = Vec<T>::N, U = D / (2 * N);
     const bool even = a.interleaved || a.rot / 2 % N == 0;
-    if (!rows || !(even || apart)) {
+    if (!rows) {
         const int64_t n = B * a.L * (D / 2);
         k_rotary_pairs<T, D><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(q, k, q_out, k_out, a, n);
         return launched();
@@ -195,12 +195,11 @@ int rotary(const void *q, const void *k, void *q_out, void *k_out, const double 
     cudaGetLastError();
     const T *tq = static_cast<const T *>(q), *tk = static_cast<const T *>(k);
     T *oq = static_cast<T *>(q_out), *ok = static_cast<T *>(k_out);
-    const bool apart = !q_in && !k_in;
     const bool rows = row_aligned(q, a.sq, es) && (!k || row_aligned(k, a.sk, es));
     switch (d) {
-    case 32: return launch_rotary<T, 32>(tq, tk, oq, ok, a, B, rows, apart, st);
-    case 64: return launch_rotary<T, 64>(tq, tk, oq, ok, a, B, rows, apart, st);
-    default: return launch_rotary<T, 128>(tq, tk, oq, ok, a, B, rows, apart, st);
+    case 32: return launch_rotary<T, 32>(tq, tk, oq, ok, a, B, rows, st);
+    case 64: return launch_rotary<T, 64>(tq, tk, oq, ok, a, B, rows, st);
+    default: return launch_rotary<T, 128>(tq, tk, oq, ok, a, B, rows, st);
     }
 }
 
@@ -299,7 +298,8 @@ int launch_decode(const T *q, const T *k, const T *v, T *kp, T *vp, float *weigh
     int64_t chunks = 1;
     if (weights)   // no more CTAs than are resident at once (they all wait); a chunk loops over its rows
         chunks = std::max<int64_t>(1, std::min((most_rows + kJoinRows - 1) / kJoinRows, kSplitCtas / units));
-    return launched(launch_early(k_paged_join<T, D>, dim3((unsigned)units, (unsigned)chunks), kJoinThreads,
+    const auto join = D < 128 && units > kSplitCtas ? k_paged_join<T, D, D < 128 ? 3 : 2> : k_paged_join<T, D, 2>;
+    return launched(launch_early(join, dim3((unsigned)units, (unsigned)chunks), kJoinThreads,
                                  dc.M ? (size_t)4 * dc.hg * D * 4 : 0, st, q,
                                  weights, out, a, dc, k ? 1 : 0));
 }

@@ -578,11 +578,15 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
 // before the wait for the split kernel: the memory's part of chunk 0, and with weights the rows'
 // places and what they have so far.  Then chunk 0 joins the pieces, gates and writes the output,
 // and every chunk adds its rows' normalised weights from the kept scores.
+// BLOCKS to an SM: two leave the registers that keep most loads in flight (d = 128, 256 units with
+// memory and weights: 51 us for the step against 55 with three; 504 units of up to three rows, fp32:
+// 28 against 34); three where a unit's memory is small and two would not hold all units at once
+// (d = 64, 432 units of one or two rows: 17 against 20).
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 1024;      // rows of a chunk
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads)
+template <typename T, int D, int BLOCKS>
+__global__ void __launch_bounds__(kJoinThreads, BLOCKS)
 k_paged_join(const T *__restrict__ q, float *weights, T *__restrict__ out, PageArgs a, DecodeArgs dc, int extra)
 {
     constexpr int TR = DecodeTile<T, D>::TR, NT = kJoinThreads, NW = NT / 32, C4 = D / 4, PER = kJoinRows / NT;

@@ -99,22 +99,27 @@ struct Vec {
 
 // Bandwidth is the bound: every element is read and written once (40 heads of 32768 tokens, d = 128,
 // bf16, read token by token: 671 MB in 108 us, 6.2 TB/s; fp32 gradients at positions near a million
-// 537 MB in 85 us, 6.3 TB/s; one element at a time took 260 and 131 us).  A thread owns two 16-byte
+// 537 MB in 85 us, 6.3 TB/s; one element at a time took 260 and 131 us; 18 of 64 channels in halves of
+// nine, 457 MB in 81 us, 5.6 TB/s, against 164 with partners fetched one by one).  A thread owns two 16-byte
 // vectors of a token's row and applies its turns, formed once, to its heads, four heads' loads
 // in flight at a time.  The vectors are
 //   kHalves:  channels c and c + rot/2 (rot/2 a whole number of vectors), or two copied ones;
 //   kPairs:   neighbours, each holding whole pairs (interleaved);
-//   kRagged:  neighbours, partners read one by one (rot/2 cuts a vector; not in place, where a
-//             partner may have been written already).
+//   kRagged:  neighbours; rot/2 cuts a vector, so the turned ones pass through shared memory, where
+//             the row's threads (of one warp: it may still be rotated in place) share its pairs.
 enum RotaryForm { kHalves, kPairs, kRagged };
 
 template <typename T, int D, int FORM>
 __global__ void __launch_bounds__(256)
 k_rotary_rows(const T *q, const T *k, T *q_out, T *k_out, RotaryArgs a, int64_t n, int per)
 {
-    constexpr int N = Vec<T>::N, U = D / (2 * N), NB = 4, NC = FORM == kRagged ? 2 * N : N;
+    constexpr int N = Vec<T>::N, U = D / (2 * N), NB = 4;
+    static_assert(32 % U == 0, "a row lies in one warp");
+    // rows of four heads; 16 bytes between rows put a warp's rows in different banks
+    constexpr int ROW = 2 * U + 1, SLOT = 256 / U * ROW;
+    __shared__ uint4 s_row[FORM == kRagged ? NB * SLOT : 1];
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n) return;
+    if (i >= n) return;                                    // whole rows (n is a multiple of U)
     const int u = (int)(i % U), half = a.rot / 2;
     const int64_t bt = i / U, b = bt / a.L, t = bt % a.L;
     int c1 = 2 * u * N, c2 = c1 + N;
@@ -124,19 +129,21 @@ k_rotary_rows(const T *q, const T *k, T *q_out, T *k_out, RotaryArgs a, int64_t 
         c1 = turned ? u * N : a.rot + 2 * (u - half / N) * N;
         c2 = turned ? c1 + half : c1 + N;
     }
-    float2 cs[NC];
+    const int64_t rest = n - (i - (threadIdx.x & 31));     // this warp's threads that have a row
+    const unsigned lanes = rest >= 32 ? 0xffffffffu : (1u << rest) - 1;
+    float2 cs[N];
 #pragma unroll
-    for (int e = 0; e < NC; ++e) {
+    for (int e = 0; e < N; ++e) {
         cs[e] = make_float2(1.f, 0.f);
         if (FORM == kHalves) {
             if (turned) cs[e] = turn_of(a, bt, t, c1 + e);
         } else if (FORM == kPairs) {
             if (c1 + 2 * e < a.rot) cs[e] = turn_of(a, bt, t, c1 / 2 + e);
-        } else if (c1 + e < a.rot) {
-            cs[e] = turn_of(a, bt, t, c1 + e < half ? c1 + e : c1 + e - half);
-            if (c1 + e < half) cs[e].y = -cs[e].y;         // y = x cos + partner * (+-sin)
+        } else if (u + e * U < half) {
+            cs[e] = turn_of(a, bt, t, u + e * U);
         }
     }
+    uint4 *row = s_row + (FORM == kRagged ? threadIdx.x / U * ROW : 0);
     const int h1 = min(((int)blockIdx.y + 1) * per, a.H + a.Hkv);
     for (int h0 = blockIdx.y * per; h0 < h1; h0 += NB) {
         uint4 v[NB][2];
@@ -147,10 +154,37 @@ k_rotary_rows(const T *q, const T *k, T *q_out, T *k_out, RotaryArgs a, int64_t 
                 v[j][0] = *reinterpret_cast<const uint4 *>(x + c1);
                 v[j][1] = *reinterpret_cast<const uint4 *>(x + c2);
             }
+        if constexpr (FORM == kRagged) {
+            __syncwarp(lanes);                             // the last heads' vectors have been read
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                if (h0 + j < h1 && c1 < a.rot) row[j * SLOT + 2 * u] = v[j][0];
+                if (h0 + j < h1 && c2 < a.rot) row[j * SLOT + 2 * u + 1] = v[j][1];
+            }
+            __syncwarp(lanes);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const int c = u + e * U;
+                if (c < half)
+#pragma unroll
+                    for (int j = 0; j < NB; ++j) {
+                        T *x = reinterpret_cast<T *>(row + j * SLOT) + c;
+                        const float x1 = ld_f(x), x2 = ld_f(x + half);
+                        st_f(x, x1 * cs[e].x - x2 * cs[e].y);
+                        st_f(x + half, x2 * cs[e].x + x1 * cs[e].y);
+                    }
+            }
+            __syncwarp(lanes);
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                if (c1 < a.rot) v[j][0] = row[j * SLOT + 2 * u];
+                if (c2 < a.rot) v[j][1] = row[j * SLOT + 2 * u + 1];
+            }
+        }
 #pragma unroll
         for (int j = 0; j < NB; ++j)
             if (h0 + j < h1) {
-                if (turned) {
+                if (FORM != kRagged && turned) {
                     float x1[N], x2[N], y1[N], y2[N];
                     Vec<T>::get(v[j][0], x1);
                     Vec<T>::get(v[j][1], x2);
@@ -160,29 +194,19 @@ k_rotary_rows(const T *q, const T *k, T *q_out, T *k_out, RotaryArgs a, int64_t 
                             y1[e] = x1[e] * cs[e].x - x2[e] * cs[e].y;
                             y2[e] = x2[e] * cs[e].x + x1[e] * cs[e].y;
                         }
-                    } else if (FORM == kPairs) {
+                    } else {
 #pragma unroll
                         for (int e = 0; e < N / 2; ++e) {
-                            const float2 w1 = cs[e], w2 = cs[(e + N / 2) % NC];
+                            const float2 w1 = cs[e], w2 = cs[e + N / 2];
                             const bool on1 = c1 + 2 * e < a.rot, on2 = c2 + 2 * e < a.rot;
                             y1[2 * e] = on1 ? x1[2 * e] * w1.x - x1[2 * e + 1] * w1.y : x1[2 * e];
                             y1[2 * e + 1] = on1 ? x1[2 * e + 1] * w1.x + x1[2 * e] * w1.y : x1[2 * e + 1];
                             y2[2 * e] = on2 ? x2[2 * e] * w2.x - x2[2 * e + 1] * w2.y : x2[2 * e];
                             y2[2 * e + 1] = on2 ? x2[2 * e + 1] * w2.x + x2[2 * e] * w2.y : x2[2 * e + 1];
                         }
-                    } else {
-                        const T *x = rotary_in(q, k, a, b, t, h0 + j);
-                        auto turn = [&](float y, int c, float2 w) {
-                            return c < a.rot ? y * w.x + ld_f(x + (c < half ? c + half : c - half)) * w.y : y;
-                        };
-#pragma unroll
-                        for (int e = 0; e < N; ++e) {
-                            y1[e] = turn(x1[e], c1 + e, cs[e]);
-                            y2[e] = turn(x2[e], c2 + e, cs[(e + N) % NC]);
-                        }
                     }
                     v[j][0] = Vec<T>::put(y1);
-                    v[j][1] = FORM != kHalves && c2 >= a.rot ? v[j][1] : Vec<T>::put(y2);
+                    if (FORM == kHalves || c2 < a.rot) v[j][1] = Vec<T>::put(y2);
                 }
                 T *y = rotary_out<T, D>(q_out, k_out, a, b, t, h0 + j);
                 *reinterpret_cast<uint4 *>(y + c1) = v[j][0];
@@ -191,8 +215,8 @@ k_rotary_rows(const T *q, const T *k, T *q_out, T *k_out, RotaryArgs a, int64_t 
     }
 }
 
-// Rows off 16-byte boundaries, and ragged halves in place: one thread per (batch, token, pair or
-// pair of copied channels), which alone reads and writes that pair in every head.
+// Rows off 16-byte boundaries: one thread per (batch, token, pair or pair of copied channels), which
+// alone reads and writes that pair in every head.
 template <typename T, int D>
 __global__ void __launch_bounds__(256)
 k_rotary_pairs(const T *q, const T *k, T *q_out, T *k_out, RotaryArgs a, int64_t n)

@@ -304,6 +304,23 @@ def test_rotary_copies_channels_that_no_pair_has():
     assert np.isinf(row[20]) and np.isfinite(np.delete(row, 20)).all()
 
 
+@pytest.mark.parametrize("d,rot,L,dt", [(64, 34, 7, torch.bfloat16), (128, 34, 301, torch.bfloat16),
+                                        (64, 18, 5, torch.float32), (32, 10, 1, torch.bfloat16),
+                                        (128, 6, 33, torch.float32)])
+def test_ragged_halves_in_place(d, rot, L, dt):
+    """Halves that cut a vector: in place as out of place, and against the definition."""
+    q, k = normal((2, 5, L, d), dt, 1), normal((2, 2, L, d), dt, 2)
+    freq, _ = rotary_frequencies(rot)
+    qo, ko = binding.rotary(q, k, freq, start=77)
+    for b, h, t in ((0, 0, 0), (1, 4, L - 1), (0, 2, L // 2)):
+        want = ref.rotate(f64(q[b, h, t]), 77 + t, f64(freq), False)
+        half = 2.0 ** -8 if dt == torch.bfloat16 else 2.0 ** -24
+        assert np.all(np.abs(f64(qo[b, h, t]) - want) <= 8 * 2.0 ** -24 * 12 + half * np.abs(want))
+    q2, k2 = q.clone(), k.clone()
+    binding.rotary(q2, k2, freq, start=77, q_out=q2, k_out=k2)
+    assert torch.equal(q2, qo) and torch.equal(k2, ko)
+
+
 def test_nan_in_a_cached_row_reaches_its_head_alone():
     c = Cache(2, 2, 64, 8, 40, "bf16", weights=False)
     c.fill([30, 35], 11)
