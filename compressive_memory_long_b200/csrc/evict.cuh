@@ -25,6 +25,7 @@ struct EvictArgs {
     int *gone;                   // [B, Hkv, gone_stride] evicted rows (with a memory)
     int64_t gone_stride;
     int64_t B;
+    int fold_rows;               // of a tile of the fold
     float *part_M, *part_z;      // [slots, D * D], [slots, kFoldLoaders, D]
 };
 
@@ -278,14 +279,17 @@ constexpr int kFoldLoaders = 16, kFoldReaders = 8;
 // 28 warps, launched with 72 registers a thread (64512 in all); the loaders go down to 64 and the
 // issuing warpgroup to 24, which gives the readers their 104.
 constexpr int kFoldThreads = 32 * (kFoldLoaders + kFoldReaders + 4);
-constexpr int kFoldRows = 256;       // rows of a tile: one reading of the accumulators
+// Rows of a tile (one reading of the accumulators): many, or two stages where no head evicts more
+// than kFoldFew, since a tile's stages pass through the pipeline whether they have rows or not (36
+// evicted rows, fp32, the whole call: 15.5 us against 20).
+constexpr int kFoldRows = 256, kFoldFew = 512;
 
-template <typename T, int D>
+template <typename T, int D, bool FEW>
 struct FoldTile {
     static constexpr bool kWide = sizeof(T) == 4;
     static constexpr int VP = kWide ? 3 : 1;               // parts of v
     static constexpr int HALF = kWide ? 32 : 64;           // rows of a stage
-    static constexpr int SUB = kFoldRows / HALF;           // stages of a tile
+    static constexpr int ROWS = FEW ? 2 * HALF : kFoldRows, SUB = ROWS / HALF;   // rows and stages of a tile
     static constexpr int KB = 2 * HALF * 128;              // bytes of a part: two blocks of 64 columns
     // Staged parts, two deep (fp32: v's parts with them; bf16: v as it is, four deep), then the
     // rows as they arrive, three deep.
@@ -324,11 +328,11 @@ __device__ __forceinline__ void split3(uint64_t xy, uint32_t (&p)[3])
     }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool FEW>
 __global__ void __launch_bounds__(kFoldThreads, 1)
 k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageArgs a, EvictArgs e, float *M)
 {
-    using Tile = FoldTile<T, D>;
+    using Tile = FoldTile<T, D, FEW>;
     constexpr int CPR = Tile::CPR, LD = Tile::LD, E = Tile::E, SUB = Tile::SUB, HALF = Tile::HALF, VP = Tile::VP, ST = 2;
     extern __shared__ unsigned char s_raw[];
     __shared__ __align__(8) uint64_t full[ST], empty[ST], tfull[2], tempty[2], drained;
@@ -342,7 +346,7 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
     auto rows_of = [&](int64_t b) { return (int64_t)max(0, cached_rows(a, b) - e.budget); };
     Walk first;
     int64_t t0, t1;
-    share_begin<kFoldCtas, kFoldThreads, 0>(rows_of, e.B, a.Hkv, kFoldRows, s_share, t0, t1, first);
+    share_begin<kFoldCtas, kFoldThreads, 0>(rows_of, e.B, a.Hkv, Tile::ROWS, s_share, t0, t1, first);
     if (t0 >= t1) {                     // the whole CTA
         asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
@@ -386,11 +390,11 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
         auto take_row = [&] {
             r1 = -1;
             if (t_ahead <= 0) return;
-            const int j = ahead.tile * kFoldRows + lane / LR * HALF + warp * LR + lane % LR;
+            const int j = ahead.tile * Tile::ROWS + lane / LR * HALF + warp * LR + lane % LR;
             b1 = ahead.b;
             kvh1 = ahead.kh;
             if (lane < SUB * LR && j < ahead.n) r1 = e.gone[((int64_t)b1 * a.Hkv + kvh1) * e.gone_stride + j];
-            walk_next<0>(ahead, rows_of, a.Hkv, e.B, kFoldRows);
+            walk_next<0>(ahead, rows_of, a.Hkv, e.B, Tile::ROWS);
             --t_ahead;
         };
         auto take_page = [&] {
@@ -540,7 +544,7 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
                     zs[x] = 0;
                 }
             }
-            walk_next<0>(at, rows_of, a.Hkv, e.B, kFoldRows);
+            walk_next<0>(at, rows_of, a.Hkv, e.B, Tile::ROWS);
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
     } else if (warp < kFoldLoaders + kFoldReaders) {
@@ -600,7 +604,7 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
 #pragma unroll
                 for (int i = 0; i < NC / 2; ++i) acc[i] = 0;
             }
-            walk_next<0>(at, rows_of, a.Hkv, e.B, kFoldRows);
+            walk_next<0>(at, rows_of, a.Hkv, e.B, Tile::ROWS);
         }
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 24;");
@@ -774,9 +778,9 @@ k_evict_finish(T *k_pages, T *v_pages, float *weights, PageArgs a, EvictArgs e, 
         const int64_t unit = blockIdx.x / parts, b = unit / a.Hkv;
         const int kvh = (int)(unit % a.Hkv);
         auto rows_of = [&](int64_t i) { return (int64_t)max(0, cached_rows(a, i) - e.budget); };
-        const int64_t nt = share_tiles<0>(rows_of(b), kFoldRows);
+        const int64_t nt = share_tiles<0>(rows_of(b), e.fold_rows);
         int64_t before;
-        const int64_t total = a.Hkv * share_count<256, 0>(rows_of, e.B, kFoldRows, b, s_share, before);
+        const int64_t total = a.Hkv * share_count<256, 0>(rows_of, e.B, e.fold_rows, b, s_share, before);
         asm volatile("griddepcontrol.wait;" ::: "memory");
         if (nt == 0) return;
         const int64_t s = before * a.Hkv + kvh * nt;

@@ -399,8 +399,18 @@ EvictSpace evict_space(int64_t B, int64_t Hkv, int64_t d, int64_t page, int64_t 
     return s;
 }
 
+template <typename T, int D, bool FEW>
+int launch_fold(const T *kp, const T *vp, const PageArgs &a, EvictArgs &e, float *M, cudaStream_t st)
+{
+    using Tile = FoldTile<T, D, FEW>;
+    e.fold_rows = Tile::ROWS;
+    if (!opt_in_smem<k_evict_fold<T, D, FEW>>(Tile::SMEM)) return INFINI_ERR_CUDA;
+    TraceScope trace("evict_fold", st);
+    return launched(launch_early(k_evict_fold<T, D, FEW>, dim3(kFoldCtas), kFoldThreads, Tile::SMEM, st, kp, vp, a, e, M));
+}
+
 template <typename T, int D>
-int launch_evict(T *kp, T *vp, float *weights, const PageArgs &a, const EvictArgs &e, float *M, float *z,
+int launch_evict(T *kp, T *vp, float *weights, const PageArgs &a, EvictArgs e, float *M, float *z,
                  int64_t units, int64_t most_rows, cudaStream_t st)
 {
     // a cluster while that gives no more CTAs than SMs and each has 2048 rows at the least
@@ -425,13 +435,9 @@ int launch_evict(T *kp, T *vp, float *weights, const PageArgs &a, const EvictArg
         if (rc != INFINI_OK) return rc;
     }
     if (M && e.gone) {
-        if (!opt_in_smem<k_evict_fold<T, D>>(FoldTile<T, D>::SMEM)) return INFINI_ERR_CUDA;
-        {
-            TraceScope trace("evict_fold", st);
-            const int rc = launched(launch_early(k_evict_fold<T, D>, dim3(kFoldCtas), kFoldThreads,
-                                                 FoldTile<T, D>::SMEM, st, kp, vp, a, e, M));
-            if (rc != INFINI_OK) return rc;
-        }
+        const int rc = most_rows - e.budget <= kFoldFew ? launch_fold<T, D, true>(kp, vp, a, e, M, st)
+                                                         : launch_fold<T, D, false>(kp, vp, a, e, M, st);
+        if (rc != INFINI_OK) return rc;
     }
     TraceScope trace("evict_finish", st);
     const int blocks = (e.budget + RowTile<T, D>::ROWS - 1) / RowTile<T, D>::ROWS;
