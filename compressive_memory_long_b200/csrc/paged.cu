@@ -285,7 +285,7 @@ template <typename T, int D, int GT>
 int launch_decode(const T *q, const T *k, const T *v, T *kp, T *vp, float *weights, T *out, const PageArgs &a,
                   const DecodeArgs &dc, int64_t most_rows, cudaStream_t st)
 {
-    constexpr size_t smem = kSplitWarps * kStages * (8192 + DecodeTile<T, D>::R * 8) + 2 * GT * D * 4;
+    constexpr size_t smem = kSplitWarps * kStages * (8192 + DecodeTile<T, D>::R * 8) + decode_sums<T>(GT) * GT * D * 4;
     if (!opt_in_smem<k_paged_split<T, D, GT>>(smem)) return INFINI_ERR_CUDA;
     {
         TraceScope trace("paged_split", st);
@@ -311,8 +311,9 @@ int pick_decode(const T *q, const T *k, const T *v, T *kp, T *vp, float *weights
     if constexpr (sizeof(T) == 4) {   // as many heads at a time as there are
         if (dc.hg == 1) return launch_decode<T, D, 1>(q, k, v, kp, vp, weights, out, a, dc, most_rows, st);
         if (dc.hg == 2) return launch_decode<T, D, 2>(q, k, v, kp, vp, weights, out, a, dc, most_rows, st);
-        if (dc.hg <= 4) return launch_decode<T, D, 4>(q, k, v, kp, vp, weights, out, a, dc, most_rows, st);
     }
+    // (bf16: the three parts of up to four heads fill one product's rows)
+    if (dc.hg <= 4) return launch_decode<T, D, 4>(q, k, v, kp, vp, weights, out, a, dc, most_rows, st);
     return launch_decode<T, D, 8>(q, k, v, kp, vp, weights, out, a, dc, most_rows, st);
 }
 

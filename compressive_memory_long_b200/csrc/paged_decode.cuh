@@ -47,6 +47,13 @@ struct DecodeTile {
     static __device__ __forceinline__ int swz(int r) { return CPR >= 8 ? (r & 7) : ((r >> 1) & 3); }
 };
 
+// Warps whose sums of a piece lie side by side: as many as the eight-head tile's shared memory holds.
+template <typename T>
+constexpr int decode_sums(int GT)
+{
+    return sizeof(T) == 2 && GT == 4 ? 4 : 2;
+}
+
 __device__ __forceinline__ int64_t unit_rows(const PageArgs &a, int64_t b, int extra)
 {
     const int len = cached_rows(a, b);
@@ -139,13 +146,16 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two values as bf16 pairs hi and lo with hi + lo = x to 2^-17 of it.
-__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo)
+// Two values as three bf16 pairs whose sum is x to 2^-25 of it.
+__device__ __forceinline__ void parts3(float x, float y, uint32_t (&p)[3])
 {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-    const __nv_bfloat162 l = __floats2bfloat162_rn(x - __bfloat162float(h.x), y - __bfloat162float(h.y));
-    hi = *reinterpret_cast<const uint32_t *>(&h);
-    lo = *reinterpret_cast<const uint32_t *>(&l);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        p[i] = *reinterpret_cast<const uint32_t *>(&h);
+        x -= __bfloat162float(h.x);
+        y -= __bfloat162float(h.y);
+    }
 }
 
 // ---- the split kernel ---------------------------------------------------------------------------
@@ -157,12 +167,16 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
 // 0.65 ms with 32-bit positions), and a piece's q, new row, frequencies and first pages travel
 // together.
 //
-// bf16: products on mma.sync m16n8k16 with the query heads as the 16 rows: rows 0-7 hold eight
-// heads' high bf16 part and rows 8-15 their low part (q after rotation, and the weights e^(s-m),
-// are 32-bit values).  Both parts of a head land in one thread, which adds them: the split costs
-// no instruction, and eight heads are the tile.  The tensor rate is no bound here (104 TFLOP/s
-// at full read bandwidth, 17% of the pipe), and a tcgen05 tile of 128 rows would be padding but for
-// eight of them, with its operands' way through shared memory and TMEM on top.
+// bf16: products on mma.sync m16n8k16 with the query heads as the 16 rows.  q after rotation and the
+// weights e^(s-m) are 32-bit values and enter as three bf16 parts each (two would leave 2^-17 of
+// them, which turns the rounding of one output in a thousand and shows in the kept weights).  Up to
+// four heads: rows 0-3 hold their first parts, 8-11 the second, 4-7 the third; a head's first two land
+// in one thread, which adds the third from the lane 16 further (250000 rows of 8 key/value heads, d =
+// 128: 157 us, 160 with two parts).  Up to eight: rows 0-7 and 8-15 hold the first two, and a second
+// product, its rows 8-15 zero, adds the third (174 us, 163 with two parts).
+// The tensor rate is no bound here (four heads: 104 TFLOP/s of useful products at full read bandwidth),
+// and a tcgen05 tile of 128 rows would be padding but for eight of them, with its operands' way through
+// shared memory and TMEM on top.
 //
 // fp32: on the CUDA cores, exactly; GT query heads at a time.  A lane forms a quarter of one
 // row's dot products, and a float4 column of the values' sum.
@@ -175,6 +189,8 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
     constexpr bool kMma = sizeof(T) == 2;
     constexpr int CPR = Tile::CPR, R = Tile::R, TR = Tile::TR, RL = Tile::RL, NT = 32 * kSplitWarps;
     constexpr int NO = D / 8;                              // mma: accumulator tiles of 8 channels
+    constexpr int SUMS = decode_sums<T>(GT);
+    constexpr bool kPack = kMma && GT == 4;                // mma: a head's three parts in one product
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float s_m[kSplitWarps][8], s_l[kSplitWarps][8];
     __shared__ __align__(16) T s_new[2][D];
@@ -183,8 +199,8 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
 
     unsigned char *stages = smem;                                                // [warp][stage][8 KB]
     float *sq = reinterpret_cast<float *>(smem + kSplitWarps * kStages * 8192);   // [GT][D]
-    float *s_o = sq;                                                             // [2][GT][D], over sq at a piece's end
-    int64_t *s_base = reinterpret_cast<int64_t *>(sq + 2 * GT * D);             // [warp][stage][R]
+    float *s_o = sq;                                                             // [SUMS][GT][D], over sq at a piece's end
+    int64_t *s_base = reinterpret_cast<int64_t *>(sq + SUMS * GT * D);             // [warp][stage][R]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int extra = k ? 1 : 0, KH = a.Hkv * dc.HT;
@@ -313,7 +329,13 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
     const float sl2 = rsqrtf((float)D) * 1.4426950408889634f;
     float m[kMma ? 1 : GT], l[kMma ? 1 : GT];
     float o[kMma ? NO : GT][4];
-    uint32_t qa[kMma ? D / 16 : 1][4];
+    uint32_t qa[kMma ? D / 16 : 1][4], qc[kMma && !kPack ? D / 16 : 1][2];   // first two parts of q, the third
+    const bool third = kPack && lane >= 16;                // this lane's rows: third parts, and none
+    const uint32_t third_bits = third ? 0xffffffffu : 0u;
+    auto place = [&](const uint32_t (&p)[3], uint32_t &top, uint32_t &bottom) {
+        top = (p[2] & third_bits) | (p[0] & ~third_bits);
+        bottom = p[1] & ~third_bits;
+    };
     int stage = 0;
 
     for (bool begins = true, first = true; left > 0;) {
@@ -326,12 +348,16 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
             rows.store(GT, dc, sq, s_new[0], s_new[1]);
             __syncthreads();
             if constexpr (kMma) {
-                const float *row = sq + (lane >> 2) * D + (lane & 3) * 2;
+                const float *row = sq + ((lane >> 2) & (GT - 1)) * D + (lane & 3) * 2;
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    split2(row[i * 16], row[i * 16 + 1], qa[i][0], qa[i][1]);
-                    split2(row[i * 16 + 8], row[i * 16 + 9], qa[i][2], qa[i][3]);
-                }
+                for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t p[3];
+                        parts3(row[i * 16 + 8 * e], row[i * 16 + 8 * e + 1], p);
+                        place(p, qa[i][2 * e], qa[i][2 * e + 1]);
+                        if constexpr (!kPack) qc[i][e] = p[2];
+                    }
             }
 #pragma unroll
             for (int g = 0; g < (kMma ? 1 : GT); ++g) {
@@ -385,6 +411,11 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
                     ldsm4(ka + (kr * CPR + ((2 * i + kc) ^ Tile::swz(kr))) * 16, b);
                     mma16816(i & 1 ? s2[0] : s[0], qa[i], b[0], b[1]);
                     mma16816(i & 1 ? s2[1] : s[1], qa[i], b[2], b[3]);
+                    if constexpr (!kPack) {
+                        const uint32_t c[4] = {qc[i][0], 0u, qc[i][1], 0u};
+                        mma16816(i & 1 ? s2[0] : s[0], c, b[0], b[1]);
+                        mma16816(i & 1 ? s2[1] : s[1], c, b[2], b[3]);
+                    }
                 }
                 const uint32_t live = (RL == 1 ? okay[0] : okay[rb >> 5]) >> (rb & 31);
                 float x[2][2], mx = m[0];
@@ -393,7 +424,8 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int j = n8 * 8 + (lane & 3) * 2 + e;
-                        const float y = (s[n8][e] + s2[n8][e]) + (s[n8][e + 2] + s2[n8][e + 2]);
+                        float y = (s[n8][e] + s2[n8][e]) + (s[n8][e + 2] + s2[n8][e + 2]);
+                        if constexpr (kPack) y += __shfl_xor_sync(0xffffffffu, y, 16);
                         x[n8][e] = live >> j & 1 ? y * sl2 : -INFINITY;
                         mx = fmaxf(mx, x[n8][e]);
                     }
@@ -409,13 +441,16 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 const float at = mx == -INFINITY ? 0.f : mx, corr = exp2f(m[0] - at);
-                uint32_t pa[4];
+                uint32_t pa[4], pc[2];
                 float p[2][2];
 #pragma unroll
                 for (int n8 = 0; n8 < 2; ++n8) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) p[n8][e] = exp2f(x[n8][e] - at);
-                    split2(p[n8][0], p[n8][1], pa[2 * n8], pa[2 * n8 + 1]);
+                    uint32_t w[3];
+                    parts3(p[n8][0], p[n8][1], w);
+                    place(w, pa[2 * n8], pa[2 * n8 + 1]);
+                    pc[n8] = w[2];
                 }
                 l[0] = l[0] * corr + ((p[0][0] + p[0][1]) + (p[1][0] + p[1][1]));
                 m[0] = mx;
@@ -433,6 +468,11 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
                     ldsm4_t(va + (vr * CPR + ((2 * i + vc) ^ Tile::swz(vr))) * 16, b);
                     mma16816(o[2 * i], pa, b[0], b[1]);
                     mma16816(o[2 * i + 1], pa, b[2], b[3]);
+                    if constexpr (!kPack) {
+                        const uint32_t c[4] = {pc[0], 0u, pc[1], 0u};
+                        mma16816(o[2 * i], c, b[0], b[1]);
+                        mma16816(o[2 * i + 1], c, b[2], b[3]);
+                    }
                 }
             }
         } else {
@@ -526,19 +566,21 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
                 return mx == -INFINITY ? 0.f : exp2f(s_m[w][g] - mx);
             };
 #pragma unroll
-            for (int turn = 0; turn < 2; ++turn) {         // warps 0, 1, then 2, 3 on top of them
-                if (warp / 2 == turn) {
-                    float *dst = s_o + (warp & 1) * GT * D;
+            for (int turn = 0; turn < kSplitWarps / SUMS; ++turn) {   // SUMS warps, then the others on top of them
+                if (warp / SUMS == turn) {
+                    float *dst = s_o + warp % SUMS * GT * D;
                     if constexpr (kMma) {
-                        const int g = lane >> 2;
+                        const int g = (lane >> 2) & (GT - 1);
                         const float f = share(warp, g, top(g));
 #pragma unroll
                         for (int i = 0; i < NO; ++i)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 float *y = dst + g * D + i * 8 + (lane & 3) * 2 + e;
-                                const float x = (o[i][e] + o[i][e + 2]) * f;
-                                *y = turn ? *y + x : x;
+                                float x = o[i][e] + o[i][e + 2];
+                                if constexpr (kPack) x += __shfl_xor_sync(0xffffffffu, x, 16);
+                                x *= f;
+                                if (!third) *y = turn ? *y + x : x;
                             }
                     } else {
 #pragma unroll
@@ -557,7 +599,11 @@ k_paged_split(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
             }
             const int64_t slot = cta + (int64_t)rd.b * KH + rd.kh;
             float *po = dc.part_o + slot * dc.hg * D;
-            for (int i = tid; i < heads * D; i += NT) po[i] = s_o[i] + s_o[GT * D + i];
+            for (int i = tid; i < heads * D; i += NT) {
+                float y = s_o[i] + s_o[GT * D + i];
+                if constexpr (SUMS == 4) y += s_o[2 * GT * D + i] + s_o[3 * GT * D + i];
+                po[i] = y;
+            }
             if (tid < heads) {
                 const float mx = top(tid);
                 float ls = 0.f;
