@@ -128,7 +128,8 @@ def infini_attn_test_wait_limit(cycles: int) -> int:
 
 
 def infini_attn_test_withhold_publish(on: bool) -> int:
-    """Test hook: the fused 64-token kernel's first unit per head skips its publish."""
+    """Test hook: the fused 64-token kernel's first unit per head skips its publish, the first
+    loading warp of the eviction's fold its rows."""
     return LIB.infini_attn_test_withhold_publish(1 if on else 0)
 
 

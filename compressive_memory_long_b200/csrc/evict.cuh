@@ -377,6 +377,12 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
     const uint32_t tmem = s_tmem;
     volatile int *abort = &s_abort;
     const int64_t steps = t1 - t0;
+    // A whole warp waits: lanes that saw the barrier and lanes that gave up go on the same way.  A role
+    // that gave up stops at once and signals nothing more, so that no other one takes a stage or an
+    // accumulator that is not complete.
+    auto wait_all = [&](uint64_t *bar, uint32_t parity, int where) {
+        return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort, where)) != 0;
+    };
 
     if (warp < kFoldLoaders) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
@@ -470,14 +476,14 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
         Walk at = first;
         int slot = 0;                   // s % 3
         uint32_t s = 0;                 // low bits of the stage's number
-        bool alive = true;
+        bool alive = warp > 0 || tc::g_paged_test_withhold == 0;   // (a test hook: warp 0 fills no stage)
         int64_t rest = stages;
         for (int64_t left = steps; left > 0 && alive; --left) {
 #pragma unroll
             for (int h = 0; h < SUB; ++h, ++s, --rest) {
                 // the products of stage s - 2 are done: its parts and its v are free
                 const int stage = s & 1;
-                if (rest <= stages - 2 && alive) alive = tc::mbar_wait(&empty[stage], ((s >> 1) - 1) & 1, abort, 90);
+                if (rest <= stages - 2 && !(alive = wait_all(&empty[stage], ((s >> 1) - 1) & 1, 90))) break;
                 if (rest > 2) issue((h + 2) % SUB, slot == 0 ? 2 : slot - 1, s + 2);
                 commit();
                 asm volatile("cp.async.wait_group 2;" ::: "memory");
@@ -525,6 +531,7 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
                 if (lane == 0) tc::mbar_arrive(&full[stage]);
                 slot = slot == 2 ? 0 : slot + 1;
             }
+            if (!alive) break;
             if (left == 1 || at.tile == at.nt - 1) {   // a piece ends: this warp's part of z
                 const int64_t slot = blockIdx.x + (int64_t)at.b * a.Hkv + at.kh;
 #pragma unroll
@@ -559,7 +566,7 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
         for (int64_t t = t0; t < t1; ++t) {
             const int64_t s = t - t0;
             const int buf = (int)(s & 1);
-            if (!tc::mbar_wait(&tfull[buf], (uint32_t)((s >> 1) & 1), abort, 91)) break;
+            if (!wait_all(&tfull[buf], (uint32_t)((s >> 1) & 1), 91)) break;
             tc::tc_fence_after();
             if (part * 32 < D) {
                 const uint32_t col = tmem + ((uint32_t)(part * 32) << 16) + buf * 2 * D + half * NC;
@@ -611,12 +618,13 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
       if (warp == kFoldLoaders + kFoldReaders && lane == 0) {
         constexpr uint32_t idesc = tc::idesc_bf16(128, D, 1, 1);
         uint32_t q = 0;                 // the stage's number
-        for (int64_t s = 0; s < steps; ++s) {
+        bool alive = true;
+        for (int64_t s = 0; s < steps && alive; ++s) {
             const int buf = (int)(s & 1);
             if (s >= 2 && !tc::mbar_wait(&tempty[buf], (uint32_t)(((s >> 1) - 1) & 1), abort, 92)) break;
             const uint32_t d0 = tmem + buf * 2 * D, d1 = d0 + D;
             for (int h = 0; h < SUB; ++h, ++q) {
-                if (!tc::mbar_wait(&full[q & 1], (q >> 1) & 1, abort, 93)) break;
+                if (!(alive = tc::mbar_wait(&full[q & 1], (q >> 1) & 1, abort, 93))) break;
                 tc::tc_fence_after();
                 const uint32_t sk = tc::smem_u32(base + (q & 1) * Tile::PART);
                 const uint32_t sv = Tile::kWide ? sk + 3 * Tile::KB
@@ -640,7 +648,7 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
                     }
                 tc::mma_commit(&empty[q & 1]);
             }
-            tc::mma_commit(&tfull[buf]);
+            if (alive) tc::mma_commit(&tfull[buf]);
         }
         // every product issued ends before TMEM is given back, whatever gave up before
         tc::mma_commit(&drained);

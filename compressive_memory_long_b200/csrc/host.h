@@ -25,4 +25,7 @@ int take_paged_status(bool &waits, bool &pages);
 // The bound of the paged entries' device waits, in SM cycles.
 int set_paged_wait_limit(long long cycles);
 
+// Whether the eviction's fold withholds its first loader warp's stages (a test hook).
+int set_paged_withhold(int on);
+
 }  // namespace infini

@@ -1531,7 +1531,7 @@ int infini_attn_test_withhold_publish(int on)
 {
     const int v = on ? 1 : 0;
     return cudaMemcpyToSymbol(infini::tc::g_test_withhold, &v, sizeof(v)) == cudaSuccess
-        ? INFINI_OK : INFINI_ERR_CUDA;
+        ? infini::set_paged_withhold(v) : INFINI_ERR_CUDA;
 }
 
 int infini_attn_trace_enable(int on)

@@ -37,6 +37,11 @@ int set_paged_wait_limit(long long cycles)
     return cudaMemcpyToSymbol(tc::g_paged_spin_limit, &cycles, sizeof(cycles)) == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
 }
 
+int set_paged_withhold(int on)
+{
+    return cudaMemcpyToSymbol(tc::g_paged_test_withhold, &on, sizeof(on)) == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
+}
+
 namespace {
 
 using namespace paged;

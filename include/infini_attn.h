@@ -432,7 +432,9 @@ INFINI_API int64_t infini_attn_trace_report(char *buf, int64_t len);
  *   in the fused 64-token kernel (additive rule, d = 64, N = 64, at most 64 units of 128
  *   tokens per head) skips publishing its memory aggregate, so the later units'
  *   waits for it run out: the call's outputs are then incomplete and
- *   infini_attn_device_status reports INFINI_ERR_TIMEOUT.  Nothing traps or hangs.
+ *   infini_attn_device_status reports INFINI_ERR_TIMEOUT.  Nothing traps or hangs.  In
+ *   infini_attn_paged_evict's fold the first warp of every block that loads rows loads none, with
+ *   the same end.
  * The last two copy to device variables synchronously (INFINI_ERR_CUDA if that fails); use
  * them while no call of this library is running on the device.
  */

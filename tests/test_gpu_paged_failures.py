@@ -1,0 +1,74 @@
+"""A bounded wait of the eviction's fold runs out, made to happen without a real failure: a test hook
+lets one loading warp fill no stage and the wait limit is short; every role gives up and the kernel
+returns."""
+import contextlib
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from compressive_memory_long_b200 import binding
+from tests.test_gpu_paged import Cache, evict_case, f64, ok, same_bits
+
+pytestmark = pytest.mark.gpu
+
+TIMEOUT = 5
+
+
+@contextlib.contextmanager
+def withheld():
+    assert binding.infini_attn_test_wait_limit(1 << 20) == 0      # about half a millisecond
+    assert binding.infini_attn_test_withhold_publish(True) == 0
+    try:
+        yield
+        torch.cuda.synchronize()
+    finally:
+        binding.infini_attn_test_withhold_publish(False)
+        binding.infini_attn_test_wait_limit(0)
+
+
+class Cut:
+    """Sequences of a few tiles and of many, to be cut to `budget` rows; the workspace is NaN."""
+
+    def __init__(self, dtype="bf16", lens=(3000, 130, 70, 20), Hkv=2, d=64, page=16, budget=64, recent=9):
+        self.lens, self.budget, self.recent = lens, budget, recent
+        B, extra = len(lens), -(-budget // page)
+        c = self.c = Cache(B, Hkv, d, page, max(lens), dtype, seed=4)
+        self.rows = c.fill(lens, 70)
+        more = Cache(B, Hkv, d, page, budget, dtype, seed=5)
+        self.dst = (more.table + c.P).contiguous()
+        c.k, c.v, c.w = torch.cat([c.k, more.k]), torch.cat([c.v, more.v]), torch.cat([c.w, more.w])
+        self.n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        self.M, self.z = torch.rand((B, Hkv, d, d)).cuda(), torch.rand((B, Hkv, d)).cuda()
+        self.kept = torch.empty((B, Hkv, budget), dtype=torch.int32, device="cuda")
+        self.lens_out = torch.empty(B, dtype=torch.int32, device="cuda")
+        self.sizes = (B, Hkv, d, c.k.shape[0], page, c.table.shape[1], extra, budget, recent, 0)
+        need = binding.LIB.infini_attn_paged_evict_workspace_bytes(B, Hkv, d, page, c.table.shape[1], budget, 1)
+        self.ws = torch.full((need // 4,), float("nan"), device="cuda")
+        self.fn = binding.LIB.infini_attn_paged_evict if dtype == "bf16" else binding.LIB.infini_attn_paged_evict_f32
+
+    def __call__(self):
+        p = lambda t: ctypes.c_void_p(t.data_ptr())
+        c = self.c
+        assert self.fn(p(c.k), p(c.v), p(c.w), p(c.table), p(self.n), p(self.dst), p(self.lens_out), p(self.kept),
+                       p(self.M), p(self.z), p(self.ws), self.ws.numel() * 4, *self.sizes,
+                       ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_fold_that_gives_up_ends_and_is_reported(dtype):
+    """The call ends, its selection and copies are those of any call, the status is read once, and the
+    same call afterwards is correct."""
+    x, y = Cut(dtype), Cut(dtype)
+    with withheld():
+        x()
+        status = binding.infini_attn_device_status()
+    assert status == TIMEOUT
+    ok()
+    y()
+    ok()
+    assert torch.equal(x.kept, y.kept) and torch.equal(x.lens_out, y.lens_out)
+    for a, b in ((x.c.k, y.c.k), (x.c.v, y.c.v), (x.c.w, y.c.w)):
+        assert same_bits(a, b)
+    evict_case([3000, 130, 70, 20], 2, 64, 16, 64, 9, dtype, fold=True, seed=4)
