@@ -726,6 +726,9 @@ template <int D>
 __device__ __forceinline__ void add_pieces(const PageArgs &a, const EvictArgs &e, float *M, float *z, int64_t unit,
                                            int64_t c0, int64_t c1, int part, int parts)
 {
+    // a fold that gave up left pieces unwritten: nothing is added then (threads whose views differ,
+    // since another stream's fold gives up meanwhile, part at the stores alone)
+    const bool complete = !tc::wait_status_set();
     __shared__ float4 s_sum[256];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     auto total = [&](float4 x) {         // over the eight warps; lane's sum, in warp 0
@@ -750,7 +753,7 @@ __device__ __forceinline__ void add_pieces(const PageArgs &a, const EvictArgs &e
                 x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
             }
         x = total(x);
-        if (warp == 0 && lane < D / 4) {
+        if (warp == 0 && lane < D / 4 && complete) {
             float4 *dst = reinterpret_cast<float4 *>(z + unit * D) + lane;
             const float4 y = *dst;
             *dst = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
@@ -770,7 +773,7 @@ __device__ __forceinline__ void add_pieces(const PageArgs &a, const EvictArgs &e
             x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
         }
         x = total(x);
-        if (warp == 0) *dst = make_float4(x.x + old.x, x.y + old.y, x.z + old.z, x.w + old.w);
+        if (warp == 0 && complete) *dst = make_float4(x.x + old.x, x.y + old.y, x.z + old.z, x.w + old.w);
     }
 }
 

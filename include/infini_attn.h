@@ -329,8 +329,11 @@ INFINI_API int64_t infini_attn_paged_decode_workspace_bytes(int64_t B, int64_t H
  *   workspace: infini_attn_paged_evict_workspace_bytes(B, Hkv, d, page, max_pages, budget,
  *     M != NULL): nothing without a memory; else 4 bytes for every row of the table beyond the
  *     budget and key/value head, and about (148 + B * Hkv) * d * d * 4
+ * budget may not exceed 2^30.
  * A wait of the fold's that gives up is reported as INFINI_ERR_TIMEOUT by
- * infini_attn_device_status.  budget may not exceed 2^30.
+ * infini_attn_device_status.  The rows are selected and copied all the same, and the pages of
+ * page_table still hold the others.  M then has the complete sums of some heads (folded by one block
+ * alone) and is as it was for all others; z is as it was.  Fold again from copies of M and z.
  */
 INFINI_API int infini_attn_paged_evict(void *k_pages, void *v_pages, float *weights,
                                        const int32_t *page_table, const int32_t *lens,

@@ -72,3 +72,25 @@ def test_a_fold_that_gives_up_ends_and_is_reported(dtype):
     for a, b in ((x.c.k, y.c.k), (x.c.v, y.c.v), (x.c.w, y.c.w)):
         assert same_bits(a, b)
     evict_case([3000, 130, 70, 20], 2, 64, 16, 64, 9, dtype, fold=True, seed=4)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_fold_that_gives_up_adds_no_unwritten_piece(dtype):
+    """No block completes a tile here, so M and z keep their bits (the workspace's pieces are NaN)."""
+    x = Cut(dtype)
+    M, z = x.M.clone(), x.z.clone()
+    with withheld():
+        x()
+        assert binding.infini_attn_device_status() == TIMEOUT
+    assert same_bits(x.M, M) and same_bits(x.z, z)
+    x()                                    # the same rows again, from M and z as they were
+    ok()
+    for b, n in enumerate(x.lens):
+        for h in range(2):
+            K, V, _ = (r[h] for r in x.rows[b])
+            gone = sorted(set(range(n)) - set(x.kept[b, h].tolist()))
+            f = np.where(K[gone] > 0, K[gone] + 1, np.exp(np.minimum(K[gone], 0)))
+            for got, old, add, size in ((x.M, M, f.T @ V[gone], f.T @ np.abs(V[gone])),
+                                        (x.z, z, f.sum(0), f.sum(0))):
+                assert np.all(np.abs(f64(got[b, h]) - f64(old[b, h]) - add)
+                              <= (2.0 ** -17 + (n + 8) * 2.0 ** -24) * (size + np.abs(f64(old[b, h]))))
