@@ -347,7 +347,8 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
     Walk first;
     int64_t t0, t1;
     share_begin<kFoldCtas, kFoldThreads, 0>(rows_of, e.B, a.Hkv, Tile::ROWS, s_share, t0, t1, first);
-    if (t0 >= t1) {                     // the whole CTA
+    // nothing to do, or a record of a wait that gave up has not been read yet (the whole CTA)
+    if (__syncthreads_or(t0 >= t1 || tc::wait_status_set())) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }

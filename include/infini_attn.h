@@ -333,7 +333,8 @@ INFINI_API int64_t infini_attn_paged_decode_workspace_bytes(int64_t B, int64_t H
  * A wait of the fold's that gives up is reported as INFINI_ERR_TIMEOUT by
  * infini_attn_device_status.  The rows are selected and copied all the same, and the pages of
  * page_table still hold the others.  M then has the complete sums of some heads (folded by one block
- * alone) and is as it was for all others; z is as it was.  Fold again from copies of M and z.
+ * alone) and is as it was for all others; z is as it was.  Fold again from copies of M and z.  Until
+ * the record is read, later calls fold nothing: they select and copy, and leave M and z.
  */
 INFINI_API int infini_attn_paged_evict(void *k_pages, void *v_pages, float *weights,
                                        const int32_t *page_table, const int32_t *lens,

@@ -94,3 +94,19 @@ def test_a_fold_that_gives_up_adds_no_unwritten_piece(dtype):
                                         (x.z, z, f.sum(0), f.sum(0))):
                 assert np.all(np.abs(f64(got[b, h]) - f64(old[b, h]) - add)
                               <= (2.0 ** -17 + (n + 8) * 2.0 ** -24) * (size + np.abs(f64(old[b, h]))))
+
+
+def test_an_unread_record_stops_later_folds():
+    """Until the record is read, a call without any fault folds nothing; then it folds as ever."""
+    x, y, z = Cut(), Cut(), Cut()
+    M, zz = y.M.clone(), y.z.clone()
+    with withheld():
+        x()
+    y()
+    assert binding.infini_attn_device_status() == TIMEOUT
+    ok()
+    assert same_bits(y.M, M) and same_bits(y.z, zz)
+    z.M.copy_(M), z.z.copy_(zz)
+    y(), z()
+    ok()
+    assert torch.equal(y.M, z.M) and torch.equal(y.z, z.z) and not torch.equal(y.M, M)
