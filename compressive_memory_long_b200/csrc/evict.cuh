@@ -29,6 +29,13 @@ struct EvictArgs {
     float *part_M, *part_z;      // [slots, D * D], [slots, kFoldLoaders, D]
 };
 
+// Rows of sequence b that leave each head (none of a padding entry, however negative its length).
+__device__ __forceinline__ int64_t rows_leaving(const PageArgs &a, const EvictArgs &e, int64_t b)
+{
+    const int n = cached_rows(a, b);
+    return n > e.budget ? n - e.budget : 0;
+}
+
 // Order-preserving image of a float: larger weight, larger key.  NaN sorts above everything,
 // and the two zeros are one value.
 __device__ __forceinline__ uint32_t weight_key(float w)
@@ -343,7 +350,7 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    auto rows_of = [&](int64_t b) { return (int64_t)max(0, cached_rows(a, b) - e.budget); };
+    auto rows_of = [&](int64_t b) { return rows_leaving(a, e, b); };
     Walk first;
     int64_t t0, t1;
     share_begin<kFoldCtas, kFoldThreads, 0>(rows_of, e.B, a.Hkv, Tile::ROWS, s_share, t0, t1, first);
@@ -789,7 +796,7 @@ k_evict_finish(T *k_pages, T *v_pages, float *weights, PageArgs a, EvictArgs e, 
     if (blockIdx.x < adders) {
         const int64_t unit = blockIdx.x / parts, b = unit / a.Hkv;
         const int kvh = (int)(unit % a.Hkv);
-        auto rows_of = [&](int64_t i) { return (int64_t)max(0, cached_rows(a, i) - e.budget); };
+        auto rows_of = [&](int64_t i) { return rows_leaving(a, e, i); };
         const int64_t nt = share_tiles<0>(rows_of(b), e.fold_rows);
         int64_t before;
         const int64_t total = a.Hkv * share_count<256, 0>(rows_of, e.B, e.fold_rows, b, s_share, before);

@@ -1,0 +1,40 @@
+"""Calls of the paged operators at the ends of what they take."""
+import numpy as np
+import pytest
+import torch
+
+from compressive_memory_long_b200 import binding
+from tests.test_gpu_paged import Cache, check_decode, normal, ok, run_decode, same_bits
+
+pytestmark = pytest.mark.gpu
+
+LOWEST = -2 ** 31
+
+
+@pytest.mark.parametrize("lens", [[LOWEST, 40], [40, LOWEST + 1], [LOWEST]])
+def test_the_lowest_length_is_a_padding_entry(lens):
+    """Any negative length marks one: no row of it is read, folded or written."""
+    B, Hkv, d = len(lens), 2, 64
+    c = Cache(B, Hkv, d, 8, 48, "bf16", seed=1)
+    rows = c.fill([max(n, 0) for n in lens], 10)
+    q, k = normal((B, 4, d), torch.bfloat16, 3), normal((B, Hkv, d), torch.bfloat16, 4)
+    out = run_decode(c, q, k, k, lens, weights=c.w)
+    check_decode(c, rows, q, k, k, lens, out, before_w=True)
+    binding.paged_append(k[:, :, None], k[:, :, None], c.k, c.v, c.table,
+                         torch.tensor([n + 1 if n > 0 else n for n in lens], dtype=torch.int32, device="cuda"),
+                         weights=c.w)
+    extra = Cache(B, Hkv, d, 8, 8, "bf16", seed=2)
+    pool = [torch.cat([x, y]) for x, y in zip((c.k, c.v, c.w), (extra.k, extra.v, extra.w))]
+    M, z = torch.ones((B, Hkv, d, d), device="cuda"), torch.ones((B, Hkv, d), device="cuda")
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    before = [x.clone() for x in pool]
+    lens_out, kept = binding.paged_evict(*pool, c.table, n, extra.table + c.P, budget=8, recent=2, M=M, z=z)
+    ok()
+    assert lens_out.tolist() == [min(n, 8) for n in lens]
+    for b, n in enumerate(lens):
+        if n < 0:
+            assert (kept[b] == -1).all() and (M[b] == 1).all() and (z[b] == 1).all()
+            dst = (extra.table[b] + c.P).long()
+            assert all(same_bits(x[dst], y[dst]) for x, y in zip(pool, before))
+        else:
+            assert (z[b] > 1).all()
