@@ -18,8 +18,9 @@ private:
     void *rec_ = nullptr;
 };
 
-// Reads and clears the current device's records of the paged entries: a bounded wait that gave
-// up, and page numbers or rows outside a cache.  INFINI_OK, or INFINI_ERR_CUDA if a copy failed.
+// Reads the current device's records of the paged entries: a bounded wait that gave up, and page
+// numbers or rows outside a cache.  Clears the first, and the second unless a wait is to be reported
+// before it (`waits` on entry: one of another unit).  INFINI_OK, or INFINI_ERR_CUDA if a copy failed.
 int take_paged_status(bool &waits, bool &pages);
 
 // The bound of the paged entries' device waits, in SM cycles.

@@ -1504,10 +1504,10 @@ int infini_attn_device_status(infini_stream_t stream)
     int v = 0;
     if (cudaMemcpyFromSymbol(&v, infini::tc::g_wait_status, sizeof(int)) != cudaSuccess)
         return INFINI_ERR_CUDA;
-    bool waits = false, pages = false;
+    bool waits = v != 0, pages = false;
     const int rc = infini::take_paged_status(waits, pages);
     if (rc != INFINI_OK) return rc;
-    if (v == 0 && !waits) return pages ? INFINI_ERR_PAGE : INFINI_OK;
+    if (!waits) return pages ? INFINI_ERR_PAGE : INFINI_OK;
     const int zero = 0;
     cudaMemcpyToSymbol(infini::tc::g_wait_status, &zero, sizeof(int));
     return INFINI_ERR_TIMEOUT;

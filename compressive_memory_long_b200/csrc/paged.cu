@@ -24,11 +24,11 @@ int take_paged_status(bool &waits, bool &pages)
     if (cudaMemcpyFromSymbol(&v[0], tc::g_paged_wait_status, sizeof(int)) != cudaSuccess ||
         cudaMemcpyFromSymbol(&v[1], paged::g_page_status, sizeof(int)) != cudaSuccess)
         return INFINI_ERR_CUDA;
-    if ((v[0] != 0 && cudaMemcpyToSymbol(tc::g_paged_wait_status, &zero, sizeof(int)) != cudaSuccess) ||
-        (v[1] != 0 && cudaMemcpyToSymbol(paged::g_page_status, &zero, sizeof(int)) != cudaSuccess))
-        return INFINI_ERR_CUDA;
-    waits = v[0] != 0;
+    waits |= v[0] != 0;
     pages = v[1] != 0;
+    if ((v[0] != 0 && cudaMemcpyToSymbol(tc::g_paged_wait_status, &zero, sizeof(int)) != cudaSuccess) ||
+        (pages && !waits && cudaMemcpyToSymbol(paged::g_page_status, &zero, sizeof(int)) != cudaSuccess))
+        return INFINI_ERR_CUDA;
     return INFINI_OK;
 }
 

@@ -399,7 +399,8 @@ INFINI_API int64_t infini_attn_workspace_bytes(int64_t B, int64_t Hkv, int64_t L
  * gave up stops early and leaves part of its outputs unwritten.  The record is sticky:
  * until it is read here, later launches of the waiting kernels return without work.
  * INFINI_ERR_PAGE if instead a paged entry met a page number or row outside its cache since the
- * last check (cleared too; later launches are not affected).
+ * last check (cleared too; later launches are not affected).  Where both happened, the timeout is
+ * reported first and the other record by the next call.
  */
 INFINI_API int infini_attn_device_status(infini_stream_t stream);
 

@@ -110,3 +110,14 @@ def test_an_unread_record_stops_later_folds():
     y(), z()
     ok()
     assert torch.equal(y.M, z.M) and torch.equal(y.z, z.z) and not torch.equal(y.M, M)
+
+
+def test_a_bad_page_is_reported_after_a_timeout():
+    """Both records of one call reach the caller, one at a time."""
+    x = Cut()
+    x.c.table[0, 3] = x.c.k.shape[0]                   # past the pool
+    with withheld():
+        x()
+        first = binding.infini_attn_device_status()
+    assert (first, binding.infini_attn_device_status()) == (TIMEOUT, 6)
+    ok()
