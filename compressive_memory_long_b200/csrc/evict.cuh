@@ -312,15 +312,53 @@ struct FoldTile {
     static constexpr uint32_t COLS = 4 * D;                // two buffers of two accumulators
 };
 
-// sigma of two values, as max(x, 0) + min(e^x, 1): the saturating addition is the minimum, and off
-// the pipe that the parts' conversions fill.  A NaN passes through the maximum.
+__device__ __forceinline__ uint64_t f2_twice(float x) { return tc::f2_pack(x, x); }
+
+__device__ __forceinline__ float max_nan(float x, float y)
+{
+    float z;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+    return z;
+}
+
+__device__ __forceinline__ float min_nan(float x, float y)
+{
+    float z;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+    return z;
+}
+
+// sigma of two values.  e^x is 2^h (1 + r ln 2) with h + r = x log2(e): 2^(x log2(e)) alone would be off
+// by the product's rounding, 0.7 |x| units, mostly to one side.  Keys below -200, whose e^x is 0, are
+// taken as that, so that nothing here is infinite.  A NaN passes through the maximum.
+//
+// bf16 values: h is the product with 16 bits of log2(e), exact; x the rest of it r (r^2 / 4 is lost: one
+// unit in 24 bits at x = -70).  sigma = max(x, 0) + min(e^x, 1); the saturating addition is the minimum,
+// and off the pipe that the parts' conversions fill.
+__device__ __forceinline__ uint64_t sigma2(uint32_t xy)
+{
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(xy) : "r"(0xc348c348u));                     // -200
+    const float x = __uint_as_float(xy << 16), y = __uint_as_float(xy & 0xffff0000u);
+    const uint64_t v = tc::f2_pack(x, y);
+    float h0, h1, e0, e1;
+    tc::f2_unpack(tc::f2_mul(v, f2_twice(1.44268798828125f)), h0, h1);
+    const uint64_t e = tc::f2_pack(tc::ex2(h0), tc::ex2(h1));
+    tc::f2_unpack(tc::f2_fma(e, tc::f2_mul(v, f2_twice(4.88849518e-6f)), e), e0, e1);
+    return tc::f2_add(tc::f2_pack(max_nan(x, 0.f), max_nan(y, 0.f)), tc::f2_pack(__saturatef(e0), __saturatef(e1)));
+}
+
+// fp32 values: h is the product with log2(e) rounded to 24 bits, r what either rounding left.
+// sigma = max(x, 0) + e^min(x, 0).
 __device__ __forceinline__ uint64_t sigma2(float x, float y)
 {
-    float p, q, e0, e1;
-    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(p) : "f"(x));
-    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(q) : "f"(y));
-    tc::f2_unpack(tc::f2_mul(tc::f2_pack(x, y), tc::f2_pack(1.4426950408889634f, 1.4426950408889634f)), e0, e1);
-    return tc::f2_add(tc::f2_pack(p, q), tc::f2_pack(__saturatef(tc::ex2(e0)), __saturatef(tc::ex2(e1))));
+    const uint64_t v = tc::f2_pack(max_nan(min_nan(x, 0.f), -200.f), max_nan(min_nan(y, 0.f), -200.f));
+    const uint64_t nh = tc::f2_mul(v, f2_twice(-1.4426950408889634f));
+    float h0, h1;
+    tc::f2_unpack(nh, h0, h1);
+    const uint64_t e = tc::f2_pack(tc::ex2(-h0), tc::ex2(-h1));
+    const uint64_t r = tc::f2_fma(v, f2_twice(1.925963033e-8f), tc::f2_fma(v, f2_twice(1.4426950408889634f), nh));
+    return tc::f2_add(tc::f2_pack(max_nan(x, 0.f), max_nan(y, 0.f)),
+                      tc::f2_fma(e, tc::f2_mul(r, f2_twice(0.6931471805599453f)), e));
 }
 
 // x = h + m + l in bf16 parts, to 2^-25 of it; pairs packed.
@@ -511,7 +549,7 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
                     for (int x = 0; x < E / 2; ++x) {
                         uint64_t f;
                         if constexpr (Tile::kWide) f = sigma2(__uint_as_float(w[2 * x]), __uint_as_float(w[2 * x + 1]));
-                        else f = sigma2(__uint_as_float(w[x] << 16), __uint_as_float(w[x] & 0xffff0000u));
+                        else f = sigma2(w[x]);
                         zs[x] = tc::f2_add(zs[x], f);
                         split3(f, p[x]);
                     }

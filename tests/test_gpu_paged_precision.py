@@ -81,3 +81,55 @@ def test_softmax_weights_keep_32_bits(H, Hkv, d):
     want, s = p @ V, p @ np.abs(V)
     half = 2.0 ** (np.floor(np.log2(np.abs(want) + 1e-300)) - 8)
     assert np.all(np.abs(out - want) <= half + 30 * U * s)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [128, 64, 32])
+def test_fold_of_negative_keys_channel_by_channel(d, dtype):
+    """One evicted row, keys from 3 down to -60, so M and z are sigma(k) v and sigma(k) of a channel.
+    sigma: the exponential is off by 2^-22 (4u) of it, its argument's remainder and the square of that
+    by 2u, the product with it or x + 1 by 1u: 7u.  M: parts to u/2, the lower ones' products and the two
+    accumulators add with 3u, and fp32 values come in parts to u/2 as well: 4u more."""
+    B, Hkv, n = 48, 2, 2
+    c = Cache(B, Hkv, d, 16, n, dtype, seed=d)
+    extra = Cache(B, Hkv, d, 16, 1, dtype, seed=d + 1)
+    dt = c.k.dtype
+    g = torch.Generator().manual_seed(d)
+    K = (3 - 63 * torch.rand((B, Hkv, d), generator=g)).to(dt)
+    V = torch.randn((B, Hkv, d), generator=g).to(dt)
+    first = c.table[:, 0].long()
+    c.k[first, :, 0], c.v[first, :, 0] = K.cuda(), V.cuda()
+    c.k[first, :, 1] = c.v[first, :, 1] = 1.0
+    c.w[first, :, :2] = 1.0
+    pool = [torch.cat([x, y]) for x, y in zip((c.k, c.v, c.w), (extra.k, extra.v, extra.w))]
+    M, z = torch.zeros((B, Hkv, d, d), device="cuda"), torch.zeros((B, Hkv, d), device="cuda")
+    binding.paged_evict(*pool, c.table, torch.full((B,), n, dtype=torch.int32, device="cuda"),
+                        extra.table + c.P, budget=1, recent=1, M=M, z=z)
+    ok()
+    f = ref.sigma(f64(K))
+    assert np.all(np.abs(f64(z) - f) <= 7 * U * f)
+    want = f[..., :, None] * f64(V)[..., None, :]
+    assert np.all(np.abs(f64(M) - want) <= 11 * U * np.abs(want))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_fold_of_the_largest_keys(dtype):
+    """sigma is 0 of keys far below, the key plus 1 of keys far above, and 0 of -inf; V beside them."""
+    keys = [-1e4, -3e38, float("-inf"), 1e4, 1e30, -87.0, 0.0, -0.0]
+    d, n = 32, 2
+    c, extra = Cache(1, 1, d, 16, n, dtype), Cache(1, 1, d, 16, 1, dtype)
+    k = torch.zeros(d)
+    k[:len(keys)] = torch.tensor(keys)
+    first = c.table[:, 0].long()
+    c.k[first, :, 0], c.v[first, :, 0] = k.to(c.k.dtype).cuda(), torch.tensor(0.5).to(c.k.dtype).cuda()
+    c.k[first, :, 1] = c.v[first, :, 1] = 1.0
+    c.w[first, :, :2] = 1.0
+    pool = [torch.cat([x, y]) for x, y in zip((c.k, c.v, c.w), (extra.k, extra.v, extra.w))]
+    M, z = torch.zeros((1, 1, d, d), device="cuda"), torch.zeros((1, 1, d), device="cuda")
+    binding.paged_evict(*pool, c.table, torch.tensor([n], dtype=torch.int32, device="cuda"), extra.table + c.P,
+                        budget=1, recent=1, M=M, z=z)
+    ok()
+    f = ref.sigma(f64(k.to(c.k.dtype)))
+    # e^-87 is 1.6e-38, next to the smallest number that is not subnormal: its parts are 0
+    assert np.all(np.abs(f64(z[0, 0]) - f) <= 7 * U * f)
+    assert np.all(np.abs(f64(M[0, 0]) - 0.5 * f[:, None]) <= 11 * U * 0.5 * f[:, None] + 2e-38)
