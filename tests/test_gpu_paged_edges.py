@@ -38,3 +38,24 @@ def test_the_lowest_length_is_a_padding_entry(lens):
             assert all(same_bits(x[dst], y[dst]) for x, y in zip(pool, before))
         else:
             assert (z[b] > 1).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,H,Hkv,d,edges", [
+    (40, 16, 8, 32, [1022, 1023, 1024, 1025, 2047, 2048, 2500, 0, -1, 3100]),   # 320 units, one chunk each
+    (38, 96, 8, 32, [1023, 1024, 1025, 2049, 1, 2500]),                         # groups of twelve beside that
+    (3, 12, 1, 64, [5000, 1024, 1023]),                                         # chunks of several blocks
+])
+def test_weights_of_rows_past_a_block_s_first_chunk(B, H, Hkv, d, edges, dtype):
+    """The rows of a (sequence, key/value head) are weighted a thousand at a time; where there are as many of
+    these as blocks fit the card, one block goes on to the next thousand itself."""
+    lens = [edges[i % len(edges)] for i in range(B)]
+    c = Cache(B, Hkv, d, 64, max(lens) + 1, dtype, seed=B)
+    rows = c.fill(lens, 20)
+    q, k, v = (normal((B, n, d), c.k.dtype, 30 + n) for n in (H, Hkv, Hkv))
+    out = run_decode(c, q, k, v, lens, weights=c.w)
+    ok()
+    few = [b for b in range(B) if b < len(edges)] + [B - 1]      # the loops in 64 bits take their time
+    check_decode(c, rows, q, k, v, [n if b in few else -1 for b, n in enumerate(lens)],
+                 torch.where(torch.tensor([b in few for b in range(B)], device="cuda")[:, None, None], out, 0),
+                 before_w=True)
