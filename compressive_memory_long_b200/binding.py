@@ -347,11 +347,21 @@ def backward(q, k, v, beta, M0, z0, dout, dM=None, dz=None, *, N: int, rule="lin
 # Checks, allocations and the C calls are native (csrc/py_paged.cpp): these steps take a few
 # microseconds on the GPU, less than the same checks in Python.
 
-if not os.path.exists(_build.EXT) and os.environ.get("INFINI_NO_AUTOBUILD") != "1":
-    _build.build_ext()
-from . import _paged  # noqa: E402
+class _Paged:
+    """The native entries, loaded by the first paged call: the others need no extension."""
 
-_paged.set_error(InfiniError)
+    def __getattr__(self, name):         # (only for what is not set yet)
+        entries = ("rotary", "append", "decode", "evict")
+        if name not in entries:
+            raise AttributeError(name)
+        ext = _build.load_ext()
+        ext.set_error(InfiniError)
+        for entry in entries:
+            setattr(self, entry, getattr(ext, entry))
+        return getattr(self, name)
+
+
+_paged = _Paged()
 
 
 def _on(stream, t, call, *args):
