@@ -171,7 +171,7 @@ int rotary(const void *q, const void *k, void *q_out, void *k_out, const double 
     if (!take_strides(q_strides, H, L, d, a.sq) || !take_strides(k_strides, Hkv, L, d, a.sk))
         return INFINI_ERR_INVALID_ARG;
     if (!aligned(q, es) || !aligned(k, es) || !aligned(q_out, 16) || !aligned(k_out, 16) ||
-        !aligned(freq, 16) || !aligned(positions, 16))
+        !aligned(freq, 16) || !aligned(positions, 8))
         return INFINI_ERR_INVALID_ARG;
     const int64_t qb = B * H * L * d * es, kb = B * Hkv * L * d * es;
     const int64_t qx = extent_bytes(a.sq, B, H, L, d, es), kx = k ? extent_bytes(a.sk, B, Hkv, L, d, es) : 0;
@@ -342,11 +342,12 @@ int paged_decode_step(const void *q, const void *k, const void *v, void *k_pages
         return INFINI_ERR_INVALID_ARG;
     const int64_t need = decode_workspace_bytes(B, H, Hkv, d, P, page, weights != nullptr);
     if (workspace_bytes < need || (need > 0 && !workspace)) return INFINI_ERR_INVALID_ARG;
-    for (const void *p : {q, k, v, (const void *)k_pages, (const void *)v_pages, (const void *)beta,
-                          (const void *)M, (const void *)z, (const void *)weights, (const void *)freq,
-                          (const void *)positions, (const void *)out, (const void *)workspace})
+    for (const void *p : {q, k, v, (const void *)k_pages, (const void *)v_pages, (const void *)M, (const void *)z,
+                          (const void *)weights, (const void *)freq, (const void *)out, (const void *)workspace})
         if (!aligned(p, 16)) return INFINI_ERR_INVALID_ARG;
-    if (!aligned(table, 4) || !aligned(lens, 4)) return INFINI_ERR_INVALID_ARG;
+    // read one element at a time, and often slices: a layer's gates, a step's positions
+    if (!aligned(table, 4) || !aligned(lens, 4) || !aligned(beta, 4) || !aligned(positions, 8))
+        return INFINI_ERR_INVALID_ARG;
     const int64_t es = (int64_t)sizeof(T), pool = P * Hkv * page;
     if (clash({{k_pages, pool * d * es, true}, {v_pages, pool * d * es, true}, {weights, pool * 4, true},
                {out, B * H * d * es, true}, {workspace, need, true}, {q, B * H * d * es, false},

@@ -207,8 +207,8 @@ INFINI_API int infini_attn_fold_f32(const void *k_cache, const void *v_cache, in
  *     contiguous; element alignment suffices (16-byte aligned rows are faster).  k may be NULL
  *     (with k_out): q alone.
  *   q_out, k_out: contiguous; each may be its own (contiguous) input
- *   freq [rot / 2] double (rot even, 0 <= rot <= d);  positions [B, L] int64, or NULL: token t
- *     is at start + t.  Negative positions are valid.
+ *   freq [rot / 2] double (rot even, 0 <= rot <= d);  positions [B, L] int64 (8-byte alignment), or
+ *     NULL: token t is at start + t.  Negative positions are valid.
  * The _bwd entries map the gradients of q_out, k_out to those of q, k with the same arguments
  * (the angle negated); they take the gradients in the place of q, k.
  */
@@ -252,8 +252,8 @@ INFINI_API int infini_attn_rotary_bwd_f32(const void *dq_out, const void *dk_out
  * page_table and lens are read on the device: a page number outside [0, P), or a row past the
  * table's end, is never followed.  Such a row is left out (not read, not written), and
  * infini_attn_device_status reports INFINI_ERR_PAGE.
- * page_table, lens, counts, dst_table and lens_out need 4-byte alignment, the strided k and v
- * of infini_attn_paged_append that of an element.
+ * page_table, lens, counts, dst_table, lens_out and the decode step's beta need 4-byte alignment,
+ * positions 8-byte, the strided k and v of infini_attn_paged_append that of an element.
  *
  * infini_attn_paged_append: rows lens[b] .. lens[b] + counts[b] - 1 become the first counts[b]
  * tokens of k, v [B, Hkv, T, d] (strides as for infini_attn_rotary; counts [B] int32, NULL: T

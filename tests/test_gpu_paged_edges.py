@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from compressive_memory_long_b200 import binding
+from compressive_memory_long_b200.positions import rotary_frequencies
 from tests.test_gpu_paged import Cache, check_decode, normal, ok, run_decode, same_bits
 
 pytestmark = pytest.mark.gpu
@@ -59,3 +60,22 @@ def test_weights_of_rows_past_a_block_s_first_chunk(B, H, Hkv, d, edges, dtype):
     check_decode(c, rows, q, k, v, [n if b in few else -1 for b, n in enumerate(lens)],
                  torch.where(torch.tensor([b in few for b in range(B)], device="cuda")[:, None, None], out, 0),
                  before_w=True)
+
+
+def test_slices_of_positions_and_gates():
+    """A step's positions and a layer's gates may be slices off 16 bytes, in the rotary call as well."""
+    lens, H, d = [5, 20, 33], 4, 64
+    c = Cache(3, 2, d, 16, 34, "f32", seed=7)
+    c.fill(lens, 40)
+    q, k = normal((3, H, d), torch.float32, 1), normal((3, 2, d), torch.float32, 2)
+    freq, _ = rotary_frequencies(d)
+    M, z = torch.rand((3, 2, d, d)).cuda(), torch.rand((3, 2, d)).cuda() + 1
+    positions, beta = torch.arange(4, device="cuda") * 1001, normal((H + 1,), torch.float32, 3)
+    assert positions[1:].data_ptr() % 16 == 8 and beta[1:].data_ptr() % 16 == 4
+    outs = [run_decode(c, q, k, k, lens, M=M, z=z, freq=freq, positions=p, beta=g)
+            for p, g in ((positions[1:], beta[1:]), (positions[1:].clone(), beta[1:].clone()))]
+    assert torch.equal(*outs)
+    x = normal((1, 2, 3, d), torch.float32, 4)
+    one, two = (binding.rotary(x, None, freq, positions=p)[0] for p in (positions[1:][None], positions[1:].clone()[None]))
+    assert torch.equal(one, two)
+    ok()
