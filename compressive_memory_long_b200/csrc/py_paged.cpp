@@ -120,6 +120,13 @@ int64_t whole(PyObject *o)
     return v;
 }
 
+int truth(PyObject *o)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Refused{};
+    return v;
+}
+
 float real(PyObject *o)
 {
     const double v = PyFloat_AsDouble(o);
@@ -201,7 +208,7 @@ PyObject *rotary(PyObject *, PyObject *const *a, Py_ssize_t n)
             ko = k_new.data_ptr();
         }
         const int64_t start = whole(a[5]);
-        const int inter = PyObject_IsTrue(a[6]);
+        const int inter = truth(a[6]);
         const float scale = real(a[7]);
         const auto fn = back ? (f32 ? infini_attn_rotary_bwd_f32 : infini_attn_rotary_bwd)
                              : (f32 ? infini_attn_rotary_f32 : infini_attn_rotary);
@@ -295,7 +302,7 @@ PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n)
         const double *freq = c.at<double>(a[11], "freq", kF64, {half});
         const int64_t *pos = c.at<int64_t>(a[12], "positions", kI64, {p.B});
         if (pos && a[11] == Py_None) refuse("positions without freq");
-        const int inter = PyObject_IsTrue(a[13]);
+        const int inter = truth(a[13]);
         const float scale = real(a[14]);
         at::Tensor made;
         void *out = c.at(a[15], "out", p.dt, {p.B, H, p.d});

@@ -79,3 +79,16 @@ def test_slices_of_positions_and_gates():
     one, two = (binding.rotary(x, None, freq, positions=p)[0] for p in (positions[1:][None], positions[1:].clone()[None]))
     assert torch.equal(one, two)
     ok()
+
+
+def test_a_flag_without_a_truth_value_is_refused():
+    q = normal((1, 2, 3, 32), torch.float32, 1)
+    before = q.clone()
+    freq, _ = rotary_frequencies(32)
+    with pytest.raises(ValueError):
+        binding.rotary(q, None, freq, start=5, interleaved=np.zeros(2), q_out=q)
+    assert torch.equal(q, before)
+    c = Cache(1, 2, 32, 8, 8, "f32")
+    with pytest.raises(ValueError):
+        run_decode(c, q[:, :, 0].contiguous(), None, None, [0], freq=freq, interleaved=np.zeros(2))
+    ok()
