@@ -31,15 +31,16 @@ struct RotaryArgs {
 };
 
 // cos and sin of pos * freq, times `scale`.  The product is formed in 64 bits (positions near
-// a million leave only about 4 bits of a 32-bit angle's fraction) and reduced there to
-// half turns in [-1, 1], which 32 bits hold to 2^-24.
+// a million leave only about 4 bits of a 32-bit angle's fraction) and reduced there to half turns in
+// [-1, 1]; what their rounding to 32 bits leaves, up to 2^-25, turns the result by as much.
 __device__ __forceinline__ float2 rotary_turn(double pos, double freq, float scale)
 {
     const double half = pos * freq * 0.31830988618379067154;     // angle / pi
     const double r = half - 2.0 * rint(0.5 * half);
+    const float t = (float)r, rest = (float)(r - (double)t) * 3.14159265358979f;
     float s, c;
-    sincospif((float)r, &s, &c);
-    return make_float2(c * scale, s * scale);
+    sincospif(t, &s, &c);
+    return make_float2(fmaf(-s, rest, c) * scale, fmaf(c, rest, s) * scale);
 }
 
 // The turn of pair i at this thread's position.

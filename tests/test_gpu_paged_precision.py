@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from compressive_memory_long_b200 import binding
+from compressive_memory_long_b200.positions import rotary_frequencies
 from tests import _paged_reference as ref
 from tests.test_gpu_paged import Cache, f64, normal, ok, run_decode
 
@@ -133,3 +134,24 @@ def test_fold_of_the_largest_keys(dtype):
     # e^-87 is 1.6e-38, next to the smallest number that is not subnormal: its parts are 0
     assert np.all(np.abs(f64(z[0, 0]) - f) <= 7 * U * f)
     assert np.all(np.abs(f64(M[0, 0]) - 0.5 * f[:, None]) <= 11 * U * 0.5 * f[:, None] + 2e-38)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("d,rot", [(128, 128), (64, 18), (32, 32)])
+def test_rotary_keeps_the_angle_s_last_bits(d, rot, inter):
+    """Pairs (1, 0) turn into cosine and sine themselves, both of the angle formed in 64 bits: off by one
+    unit in the last place of a 32-bit function's value (u below 1) and half of one of its correction."""
+    L, start = 4000, 1048000
+    x = torch.zeros((1, 1, L, d), device="cuda")
+    first = slice(0, rot, 2) if inter else slice(0, rot // 2)
+    second = slice(1, rot, 2) if inter else slice(rot // 2, rot)
+    x[..., first] = 1.0
+    freq, _ = rotary_frequencies(rot)
+    y, _ = binding.rotary(x, None, freq, start=start, interleaved=inter)
+    odd = torch.zeros((1, 1, L, d + 1), device="cuda")[..., 1:]            # rows off 16 bytes as well
+    odd.copy_(x)
+    assert torch.equal(binding.rotary(odd, None, freq, start=start, interleaved=inter)[0], y)
+    a = (start + np.arange(L))[:, None] * f64(freq)
+    y = f64(y[0, 0])
+    assert np.abs(y[:, first] - np.cos(a)).max() <= 1.5 * U
+    assert np.abs(y[:, second] - np.sin(a)).max() <= 1.5 * U
