@@ -402,7 +402,8 @@ def paged_append(k, v, k_pages, v_pages, page_table, lens, *, counts=None, weigh
     lens[b]+counts[b]-1 of the cache (counts [B] int32, None: T each); their weights start at 0.
 
     k_pages/v_pages [P,Hkv,page,d] (bf16 or fp32), page_table [B,max_pages] and lens [B] int32,
-    weights [P,Hkv,page] fp32 or None.  lens is left to the caller.
+    weights [P,Hkv,page] fp32 or None (only decode steps add to it).  No call changes lens: add the
+    rows yourself.
     """
     return _on(stream, k_pages, _paged.append, k, v, k_pages, v_pages, page_table, lens, counts, weights)
 
@@ -416,7 +417,7 @@ def paged_decode_step(q, k, v, k_pages, v_pages, page_table, lens, *, beta=None,
     cache arguments as for ``paged_append``.  With freq [rot/2] fp64, q and k are rotated first,
     at positions [B] int64 (None: lens).  k, v become row lens[b]; the attention spans rows
     0..lens[b].  With beta [H], M [B,Hkv,d,d] and z [B,Hkv,d] (fp32; all or none) the memory is
-    read and gated in as in the forward.  With weights, every row's softmax weight is added to
+    read, with the rotated q, and gated in as in the forward.  With weights, every row's softmax weight is added to
     it.  lens < 0 marks a padding entry: its output is 0.  Returns out [B,H,d].
     """
     return _on(stream, q, _paged.decode, q, k, v, k_pages, v_pages, page_table, lens, beta, M, z, weights,
@@ -430,7 +431,7 @@ def paged_evict(k_pages, v_pages, weights, page_table, lens, dst_table, *, budge
     of the highest accumulated weight (per key/value head; ties keep the lowest row).  The kept
     rows are copied, in order, to the pages dst_table [B,dst_pages] int32 names, which must be
     pages of their own.  With M [B,Hkv,d,d] and z [B,Hkv,d] the evicted rows are folded into the
-    memory in place.  Returns (lens_out [B], kept [B,Hkv,budget] int32: old rows, -1 padded).
+    memory in place, with the keys as the cache holds them.  Returns (lens_out [B], kept [B,Hkv,budget] int32: old rows, -1 padded).
     """
     return _on(stream, k_pages, _paged.evict, k_pages, v_pages, weights, page_table, lens, dst_table, budget,
                recent, M, z, RULES[rule], lens_out, kept)

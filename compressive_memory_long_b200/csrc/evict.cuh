@@ -8,7 +8,7 @@
 //
 // Three steps, each a kernel that may start while the one before drains: select (cluster of
 // CTAs per head, the weights read once), fold (tensor cores, the evicted rows shared out over
-// all SMs, then a reduction of the pieces), move.
+// all SMs), finish (adds the fold's pieces to the memory and moves the kept rows).
 #pragma once
 
 #include "paged.cuh"

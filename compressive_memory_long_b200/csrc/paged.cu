@@ -481,7 +481,7 @@ int paged_evict(void *k_pages, void *v_pages, float *weights, const int *table, 
         if (!aligned(p, 16)) return INFINI_ERR_INVALID_ARG;
     for (const int *p : {table, lens, dst_table, (const int *)lens_out})
         if (!aligned(p, 4)) return INFINI_ERR_INVALID_ARG;
-    // lens_out may be lens itself
+    // lens_out may not be lens: all three kernels still read lens after the first has written lens_out
     if (clash({{k_pages, pool * d * es, true}, {v_pages, pool * d * es, true}, {weights, pool * 4, true},
                {lens_out, B * 4, true}, {kept, units * budget * 4, true}, {M, units * d * d * 4, true},
                {z, units * d * 4, true}, {workspace, need, true}, {table, B * max_pages * 4, false},

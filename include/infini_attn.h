@@ -250,15 +250,16 @@ INFINI_API int infini_attn_rotary_bwd_f32(const void *dq_out, const void *dk_out
  * No entry allocates memory; all may be captured in a graph.  A workspace, where one is asked
  * for, holds nothing between calls, and calls that may overlap on the GPU need one each.
  * page_table and lens are read on the device: a page number outside [0, P), or a row past the
- * table's end, is never followed.  Such a row is left out (not read, not written), and
- * infini_attn_device_status reports INFINI_ERR_PAGE.
+ * table's end, is never followed.  Such a row is left out (not read, not written; the new row of a
+ * decode step is attended to all the same), and infini_attn_device_status reports INFINI_ERR_PAGE.
  * page_table, lens, counts, dst_table, lens_out and the decode step's beta need 4-byte alignment,
  * positions 8-byte, the strided k and v of infini_attn_paged_append that of an element.
  *
  * infini_attn_paged_append: rows lens[b] .. lens[b] + counts[b] - 1 become the first counts[b]
  * tokens of k, v [B, Hkv, T, d] (strides as for infini_attn_rotary; counts [B] int32, NULL: T
  * for every sequence; a count beyond T counts as T), and their weights 0.  T * Hkv may not
- * exceed 2^30.
+ * exceed 2^30.  Only decode steps add to weights: an eviction right behind a prompt finds ties, and
+ * keeps the lowest rows and the recent ones, unless the caller writes weights of its own.
  */
 INFINI_API int infini_attn_paged_append(const void *k, const void *v, const int64_t *k_strides,
                                         const int64_t *v_strides, void *k_pages, void *v_pages,
@@ -283,7 +284,8 @@ INFINI_API int infini_attn_paged_append_f32(const void *k, const void *v, const 
  *     and the attention spans the cached rows alone;
  *   - softmax attention of q over rows 0 .. lens[b]; a sequence without rows gives 0;
  *   - with beta, M and z (all or none): the retrieval from (M, z) with the rotated q and the
- *     gate, as in the forward; M and z are read only;
+ *     gate, as in the forward given rotated q and k (with rot > 0 the retrieval so depends on the
+ *     positions); M and z are read only;
  *   - with weights: every row's softmax weight, summed over the group's query heads, is added.
  *     The pages of a sequence must then be its own.
  * Padding entries (lens < 0) give rows of 0.
@@ -325,7 +327,8 @@ INFINI_API int64_t infini_attn_paged_decode_workspace_bytes(int64_t B, int64_t H
  *   lens_out [B]: min(lens[b], budget) (may not be lens itself)
  *   kept [B, Hkv, budget] int32: the old rows of the kept ones, ascending, -1 past the last
  *   M, z (both or none): the rows not kept are folded in, in place, as one update of the
- *     forward's rule.  INFINI_UPDATE_DELTA is not built: INFINI_ERR_UNSUPPORTED.
+ *     forward's rule, with the keys as the cache holds them (rotated ones rotated).
+ *     INFINI_UPDATE_DELTA is not built: INFINI_ERR_UNSUPPORTED.
  *   workspace: infini_attn_paged_evict_workspace_bytes(B, Hkv, d, page, max_pages, budget,
  *     M != NULL): nothing without a memory; else 4 bytes for every row of the table beyond the
  *     budget and key/value head, and about (148 + B * Hkv) * d * d * 4
