@@ -388,12 +388,13 @@ k_evict_fold(const T *__restrict__ k_pages, const T *__restrict__ v_pages, PageA
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
+    const bool given_up = tc::wait_status_set();           // (its latency lies beside that of the lengths)
     auto rows_of = [&](int64_t b) { return rows_leaving(a, e, b); };
     Walk first;
     int64_t t0, t1;
     share_begin<kFoldCtas, kFoldThreads, 0>(rows_of, e.B, a.Hkv, Tile::ROWS, s_share, t0, t1, first);
     // nothing to do, or a record of a wait that gave up has not been read yet (the whole CTA)
-    if (__syncthreads_or(t0 >= t1 || tc::wait_status_set())) {
+    if (__syncthreads_or(t0 >= t1 || given_up)) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
