@@ -277,7 +277,7 @@ k_evict_select(const float *__restrict__ weights, PageArgs a, EvictArgs e, int C
 // one thread issues the products; eight warps read the accumulators.  Reading K and V is the floor
 // (4 d bytes a row against 2 d^2 operations), 1400 cycles for a stage (bf16, d = 128).  Shared
 // memory is the bound: copies and parts move 96 KB through it and the products' operands 96 KB,
-// 1500 cycles at 128 bytes, and a stage takes 2200 (65500 rows of 8 heads: 80 us, 3.3 TB/s).
+// 1500 cycles at 128 bytes, and a stage takes 2300 (65500 rows of 8 heads: 79 us, 3.3 TB/s).
 // Tried without gain: sigma as max(k, 0) + e^min(k, 0) with the first term taken as a part (fewer
 // instructions, the same time); z as a product with a column of ones (reads sigma's parts once
 // more: 98 us).
@@ -288,7 +288,7 @@ constexpr int kFoldLoaders = 16, kFoldReaders = 8;
 constexpr int kFoldThreads = 32 * (kFoldLoaders + kFoldReaders + 4);
 // Rows of a tile (one reading of the accumulators): many, or two stages where no head evicts more
 // than kFoldFew, since a tile's stages pass through the pipeline whether they have rows or not (36
-// evicted rows, fp32, the whole call: 15.5 us against 20).
+// evicted rows, fp32, the whole call: 16 us against 20).
 constexpr int kFoldRows = 256, kFoldFew = 512;
 
 template <typename T, int D, bool FEW>

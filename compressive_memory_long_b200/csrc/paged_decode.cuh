@@ -8,8 +8,8 @@
 // The work is read bandwidth: 2 d elements per row against 4 d operations per query head.  So
 // the split kernel is one resident wave of CTAs (two per SM) that share all rows of the batch
 // evenly (share.cuh); a unit there is a (sequence, key/value head, tile of up to eight query
-// heads).  Measured (8 key/value heads, d = 128, bf16): one sequence of 1,000,003 rows 590-640 us,
-// 6.4-6.9 TB/s; 32 ragged sequences with memory and weights, 157 MB, 51 us: 7 until the first
+// heads).  Measured (8 key/value heads, d = 128, bf16): one sequence of 1,000,003 rows 590-605 us,
+// 6.8-6.9 TB/s; 32 ragged sequences with memory and weights, 157 MB, 51 us: 7 until the first
 // tiles are in, 27 for the rows, then the join; one sequence of 64 rows (d = 64) 8 us, all latency.
 #pragma once
 
@@ -172,11 +172,11 @@ __device__ __forceinline__ void parts3(float x, float y, uint32_t (&p)[3])
 // them, which turns the rounding of one output in a thousand and shows in the kept weights).  Up to
 // four heads: rows 0-3 hold their first parts, 8-11 the second, 4-7 the third; a head's first two land
 // in one thread, which adds the third from the lane 16 further (250000 rows of 8 key/value heads, d =
-// 128: 157 us, 160 with two parts).  Up to eight: rows 0-7 and 8-15 hold the first two, and a second
-// product, its rows 8-15 zero, adds the third (174 us, 163 with two parts).
-// The tensor rate is no bound here (four heads: 104 TFLOP/s of useful products at full read bandwidth),
-// and a tcgen05 tile of 128 rows would be padding but for eight of them, with its operands' way through
-// shared memory and TMEM on top.
+// 128: 157 us, 160 with two parts; d = 32, where rows are short, 4 million of 2 heads: 230, 209 with
+// two).  Up to eight: rows 0-7 and 8-15 hold the first two, and a second product, its rows 8-15
+// zero, adds the third (174 us, 163 with two parts).  The tensor rate is no bound here (104 TFLOP/s,
+// all 16 rows counted, at full read bandwidth: 18% of the pipe), and a tcgen05 tile of 128 rows would be
+// padding but for eight of them, with its operands' way through shared memory and TMEM on top.
 //
 // fp32: on the CUDA cores, exactly; GT query heads at a time.  A lane forms a quarter of one
 // row's dot products, and a float4 column of the values' sum.
