@@ -1,6 +1,6 @@
 // tc_common.cuh for the paged entries' translation unit: the device variables it defines (status
 // word, wait limit, test hook) get names of their own, since each unit has its own copy.
-// infini_attn_device_status and infini_attn_test_wait_limit see to both.
+// infini_attn_device_status and the test hooks see to both.
 #pragma once
 
 #define g_wait_status g_paged_wait_status

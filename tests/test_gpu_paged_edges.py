@@ -44,7 +44,7 @@ def test_the_lowest_length_is_a_padding_entry(lens):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("B,H,Hkv,d,edges", [
     (40, 16, 8, 32, [1022, 1023, 1024, 1025, 2047, 2048, 2500, 0, -1, 3100]),   # 320 units, one chunk each
-    (38, 96, 8, 32, [1023, 1024, 1025, 2049, 1, 2500]),                         # groups of twelve beside that
+    (76, 48, 4, 32, [1023, 1024, 1025, 2049, 1, 2500]),                         # groups of twelve, 304 units
     (3, 12, 1, 64, [5000, 1024, 1023]),                                         # chunks of several blocks
 ])
 def test_weights_of_rows_past_a_block_s_first_chunk(B, H, Hkv, d, edges, dtype):
